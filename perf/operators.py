@@ -1,0 +1,431 @@
+"""The block-scaled 8-bit cache's operators, as they are measured: the append with the position rotation, the
+single-token attention and the attention of prompt chunks.
+
+The cache is the library's `fp8b` pool: [slot][kv head] page blocks of 256 tokens.  A page block is four tiles of 64
+tokens and then the tiles' scales.  A tile is 16,384 bytes of K codes and 16,384 of V codes, all E4M3:
+
+  K, token t, dim d:  (d >> 7) * 8192 + (t >> 3) * 1024 + (t & 7) * 128 + ((((d >> 4) & 7) ^ (t & 7)) << 4) + (d & 15)
+  V, token t, dim d:  (d >> 3) * 512 + (d & 7) * 64 + (((t >> 4) ^ ((d >> 1) & 3)) << 4) + (t & 15)
+
+The scales are fp32 powers of two (or 0 for a tile of zeros) at byte 131,072: (K, V) of tile 0, of tile 1, ...; the page
+block is padded to 131,200 bytes.  A value is code * scale of its tile.
+
+Below, `run` computes each operator with elementary torch operations in fp32 from the same pool bytes; with `own` it
+makes the library's calls.
+"""
+import math
+
+import torch
+
+own = False
+
+D, PAGE, TILE, TILE_BYTES, CODES, PAGE_BYTES = 256, 256, 64, 32768, 131072, 131200
+DTYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+
+
+# ---- the cases ------------------------------------------------------------------------------------------------------
+def listed():
+    return [
+        # one decoding sequence of the 27B shape adds its newest token: the smallest append, all latency
+        dict(name="append 1x1", op="append", hq=24, hkv=4, pos0="1000", toks="1", dtype="bf16", rot=64, inter=False, qf32=True),
+        # a batch of decoding sequences at ragged positions
+        dict(name="append 64x1", op="append", hq=16, hkv=2, pos0=",".join(str(37 + 61 * i) for i in range(64)),
+             toks=",".join(["1"] * 64), dtype="bf16", rot=256, inter=False, qf32=True),
+        # a chunk of a long prompt, at an odd place, in fp16 with interleaved pairs
+        dict(name="append 513", op="append", hq=24, hkv=4, pos0="32255", toks="513", dtype="f16", rot=128, inter=True, qf32=False),
+        # whole prompts of three sequences, packed, the last one an extension: the largest append
+        dict(name="append 8.9k", op="append", hq=24, hkv=4, pos0="0,0,1111", toks="5000,17,3900", dtype="bf16", rot=256, inter=False, qf32=False),
+        # one short sequence: latency
+        dict(name="decode 1x1000", op="decode", hq=4, hkv=1, lens="1000"),
+        # the 27B shape at 32,768 tokens
+        dict(name="decode 1x32768", op="decode", hq=24, hkv=4, lens="32768"),
+        # a serving batch of ragged sequences, one a single token long
+        dict(name="decode 48 ragged", op="decode", hq=16, hkv=2,
+             lens=",".join(str(1 + (i * 389 + i * i * 7) % 9000) for i in range(48))),
+        # four long sequences of ragged lengths, the largest decode
+        dict(name="decode 4 long", op="decode", hq=24, hkv=4, lens="8192,65536,200000,262144"),
+        # drafts of a few tokens each are checked against their caches
+        dict(name="prefill 8x5", op="prefill", hq=24, hkv=4, pos0="100,2000,777,4095,64,1,3333,1500", toks="5,5,5,5,5,5,5,5", dtype="bf16"),
+        # a chunk of a long prompt: the last 512 of 32,768 tokens
+        dict(name="prefill 512 of 32768", op="prefill", hq=24, hkv=4, pos0="32256", toks="512", dtype="bf16"),
+        # chunks of different sequences in one call, fp16
+        dict(name="prefill 3 ragged", op="prefill", hq=16, hkv=2, pos0="0,5000,901", toks="1025,63,2047", dtype="f16"),
+        # a whole prompt, the largest
+        dict(name="prefill 7777", op="prefill", hq=24, hkv=4, pos0="0", toks="7777", dtype="bf16"),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["append", "decode", "prefill"])
+    hq, hkv = rng.choice([(24, 4), (16, 2), (4, 1), (12, 2), (8, 8), (7, 1), (10, 5)])
+    if op == "append":
+        n = _log(rng, 1, 64)
+        toks, left = [], 8900
+        for _ in range(n):
+            t = min(_log(rng, 1, 6000) if rng.random() < 0.5 else 1, left - (n - len(toks)))
+            toks.append(max(t, 1))
+            left -= toks[-1]
+        pos0 = [rng.choice([0, _log(rng, 1, 30000)]) for _ in range(n)]
+        return dict(op=op, hq=hq, hkv=hkv, pos0=",".join(map(str, pos0)), toks=",".join(map(str, toks)),
+                    dtype=rng.choice(["bf16", "f16", "f32"]), rot=rng.choice([0, 64, 128, 192, 256]),
+                    inter=rng.random() < 0.5, qf32=rng.random() < 0.5)
+    if op == "decode":
+        n = _log(rng, 1, 64)
+        lens, left = [], 2100000 // hkv
+        for _ in range(n):
+            lens.append(min(_log(rng, 1, 262144 if n <= 4 else 20000), max(1, left)))
+            left -= lens[-1]
+        return dict(op=op, hq=hq, hkv=hkv, lens=",".join(map(str, lens)))
+    n = _log(rng, 1, 8)
+    toks = [_log(rng, 1, 4000 // n) for _ in range(n)]
+    pos0 = [rng.choice([0, min(_log(rng, 1, 30000), 20000000 // n // t)]) for t in toks]
+    return dict(op=op, hq=hq, hkv=hkv, pos0=",".join(map(str, pos0)), toks=",".join(map(str, toks)),
+                dtype=rng.choice(["bf16", "f16", "f32"]))
+
+
+def _ints(text):
+    return [int(t) for t in text.split(",")]
+
+
+def _lens(case):
+    if case["op"] == "decode":
+        return _ints(case["lens"])
+    return [p + t for p, t in zip(_ints(case["pos0"]), _ints(case["toks"]))]
+
+
+def work(case):
+    hq, hkv, lens = case["hq"], case["hkv"], _lens(case)
+    if case["op"] == "append":
+        e = 4 if case["dtype"] == "f32" else 2
+        eo = 4 if case["qf32"] else e
+        rows = sum(_ints(case["toks"]))
+        return {"bytes": rows * D * (hq * (e + eo) + 2 * hkv * (e + 1)) + rows * case["rot"] * 4, "flops": rows * (hq + hkv) * 3 * D}
+    kv = sum(lens) * hkv * 2 * D
+    if case["op"] == "decode":
+        return {"bytes": kv + len(lens) * hq * D * (4 + 2), "flops": 4 * D * hq * sum(lens)}
+    pos0, toks = _ints(case["pos0"]), _ints(case["toks"])
+    pairs = sum(t * p + t * (t + 1) // 2 for p, t in zip(pos0, toks))
+    e = 4 if case["dtype"] == "f32" else 2
+    return {"bytes": kv + sum(toks) * hq * D * (e + 2), "flops": 4 * D * hq * pairs}
+
+
+# ---- the pool's bytes -----------------------------------------------------------------------------------------------
+def _swizzles(dev):
+    a = torch.arange(8, device=dev)
+    return a[:, None] ^ a[None, :], torch.arange(4, device=dev)[None, :] ^ ((a[:, None] >> 1) & 3)
+
+
+def _pack(k, v):
+    """Codes (uint8 [..., 64 tokens, 256 dims]) of K and V as tile bytes [..., 32768]."""
+    lead, n = k.shape[:-2], k.numel() // (TILE * D)
+    sk, sv = _swizzles(k.device)
+    r = torch.arange(8, device=k.device)[:, None]
+    k = k.reshape(n, 8, 8, 2, 8, 16).permute(0, 3, 1, 2, 4, 5)          # [dim half][token group][row][16-byte chunk][byte]
+    v = v.reshape(n, 4, 16, 32, 8).permute(0, 3, 4, 1, 2)               # [dim group][row][16-token chunk][byte]
+    return torch.cat([k[:, :, :, r, sk].reshape(n, -1), v[:, :, r, sv].reshape(n, -1)], 1).reshape(*lead, TILE_BYTES)
+
+
+def _unpack(tiles):
+    """The reverse: uint8 [..., 32768] -> K and V codes, uint8 [..., 64, 256]."""
+    lead, n = tiles.shape[:-1], tiles.numel() // TILE_BYTES
+    sk, sv = _swizzles(tiles.device)
+    r = torch.arange(8, device=tiles.device)[:, None]
+    t = tiles.reshape(n, TILE_BYTES)
+    k = t[:, :16384].reshape(n, 2, 8, 8, 8, 16)[:, :, :, r, sk].permute(0, 2, 3, 1, 4, 5).reshape(*lead, TILE, D)
+    v = t[:, 16384:].reshape(n, 32, 8, 4, 16)[:, :, r, sv].permute(0, 3, 4, 1, 2).reshape(*lead, TILE, D)
+    return k, v
+
+
+def _pow2(amax):
+    """The smallest power of two d with amax <= 448 d (0 where amax is 0)."""
+    m, e = torch.frexp(amax)
+    e = torch.where(m <= 0.875, e - 9, e - 8).clamp(-120, 118)
+    return torch.where(amax > 0, torch.ldexp(torch.ones_like(amax), e), torch.zeros_like(amax))
+
+
+def _encode(x, d):
+    """E4M3 codes (uint8) of x / d, zero where d is."""
+    y = torch.where(d > 0, x / torch.where(d > 0, d, torch.ones_like(d)), torch.zeros_like(x))
+    return y.clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+
+
+def _pool(n_pages, hkv, mul, gen):
+    """A filled pool: K normal with some strong channels, V normal with a size of its own for each tile."""
+    dev = mul.device
+    pool = torch.zeros((n_pages, hkv, PAGE_BYTES), dtype=torch.uint8, device=dev)
+    step = max(1, 400 // hkv)
+    for p in range(0, n_pages, step):
+        n = min(step, n_pages - p)
+        k = torch.randn((n, hkv, 4, TILE, D), generator=gen, device=dev) * mul[:, None, None]
+        v = torch.randn((n, hkv, 4, TILE, D), generator=gen, device=dev)
+        v *= torch.exp(0.5 * torch.randn((n, hkv, 4, 1, 1), generator=gen, device=dev))
+        dk, dv = _pow2(k.abs().amax((3, 4))), _pow2(v.abs().amax((3, 4)))
+        tiles = _pack(_encode(k, dk[..., None, None]), _encode(v, dv[..., None, None]))
+        pool[p:p + n, :, :CODES] = tiles.reshape(n, hkv, CODES)
+        pool[p:p + n, :, CODES:CODES + 32] = torch.stack([dk, dv], -1).reshape(n, hkv, 8).view(torch.uint8)
+    return pool
+
+
+def prepare(case, seed):
+    dev = "cuda"
+    gen = torch.Generator(device=dev).manual_seed(seed * 2654435761 % (1 << 62) + 17)
+    hq, hkv, lens = case["hq"], case["hkv"], _lens(case)
+    n_seq, max_pages = len(lens), max((n + PAGE - 1) // PAGE for n in lens)
+    need = [(n + PAGE - 1) // PAGE for n in lens]
+    mul = torch.ones((hkv, D), device=dev)
+    strong = torch.randint(0, D, (hkv, 4), generator=gen, device=dev)
+    mul.scatter_(1, strong, 10.0)
+    pool = _pool(sum(need), hkv, mul, gen)
+    slots = torch.randperm(sum(need), generator=gen, device=dev).to(torch.int32)
+    table = torch.full((n_seq, max_pages), -1, dtype=torch.int32, device=dev)
+    at = 0
+    for b, n in enumerate(need):
+        table[b, :n] = slots[at:at + n]
+        at += n
+    s = dict(op=case["op"], hq=hq, hkv=hkv, pool=pool, table=table, lens=lens,
+             lens_dev=torch.tensor(lens, dtype=torch.int32, device=dev))
+    if case["op"] == "decode":
+        s["q"] = torch.randn((n_seq, hq, D), generator=gen, device=dev)
+        if own:                                                  # a serving loop keeps the step's plan and one workspace
+            kvq = _lib()
+            s["cpool"] = kvq.KVPool(kvq.make_desc(1, hkv, hq, pool.shape[0], "fp8b"), pool)
+            plan, s["info"] = kvq.decode_plan(s["cpool"].desc, lens, max_pages)
+            s["plan"] = torch.from_numpy(plan).to(dev)
+            s["work"] = torch.zeros(s["info"].workspace_bytes // 4, dtype=torch.float32, device=dev)
+        return s
+    pos0, toks, dt = _ints(case["pos0"]), _ints(case["toks"]), DTYPES[case["dtype"]]
+    rows = sum(toks)
+    s.update(pos0=pos0, toks=toks, pos0_dev=torch.tensor(pos0, dtype=torch.int32, device=dev),
+             toks_dev=torch.tensor(toks, dtype=torch.int32, device=dev))
+    s["start"] = torch.zeros(n_seq + 1, dtype=torch.int32, device=dev)
+    s["start"][1:] = torch.cumsum(s["toks_dev"], 0)
+    if case["op"] == "prefill":
+        s["q"] = torch.randn((rows, hq, D), generator=gen, device=dev).to(dt)
+        if own:
+            kvq = _lib()
+            s["cpool"] = kvq.KVPool(kvq.make_desc(1, hkv, hq, pool.shape[0], "fp8b"), pool)
+            plan, s["info"] = kvq.prefill_plan(s["cpool"].desc, pos0, toks, max_pages)
+            s["plan"] = torch.from_numpy(plan).to(dev)
+            s["work"] = torch.zeros(s["info"].workspace_bytes // 4, dtype=torch.float32, device=dev)
+        return s
+    # the rows of a projection's output: q, k and v of a token side by side
+    qkv = torch.randn((rows, hq + 2 * hkv, D), generator=gen, device=dev)
+    qkv[:, hq:hq + hkv] *= mul
+    qkv = qkv.to(dt)
+    s.update(q=qkv[:, :hq], k=qkv[:, hq:hq + hkv], v=qkv[:, hq + hkv:], rot=case["rot"], inter=case["inter"],
+             q_dtype=torch.float32 if case["qf32"] else dt)
+    n_pos, half = max(lens), case["rot"] // 2
+    angle = torch.arange(n_pos, device=dev, dtype=torch.float64)[:, None] * \
+        torch.exp(-math.log(1e6) * torch.arange(half, device=dev, dtype=torch.float64) / max(half, 1))[None]
+    s["table_cs"] = torch.cat([angle.cos(), angle.sin()], 1).float()
+    if own:
+        kvq = _lib()
+        s["cpool"] = kvq.KVPool(kvq.make_desc(1, hkv, hq, pool.shape[0], "fp8b"), pool)
+    return s
+
+
+def _lib():
+    import quantized_kv_cache_17_b200 as kvq
+    return kvq
+
+
+# ---- one pass -------------------------------------------------------------------------------------------------------
+def run(s):
+    if own:
+        return _run_own(s)
+    return {"append": _append, "decode": _decode, "prefill": _prefill}[s["op"]](s)
+
+
+def _run_own(s):
+    kvq = _lib()
+    if s["op"] == "append":
+        q = kvq.kv_append_rope(s["cpool"], 0, s["k"], s["v"], s["start"], s["pos0_dev"], s["table"],
+                               cos_sin=s["table_cs"] if s["rot"] else None, interleaved=s["inter"], q=s["q"],
+                               q_out_dtype=s["q_dtype"])
+        return _cache(s), q
+    if s["op"] == "decode":
+        out = torch.empty((len(s["lens"]), s["hq"], D), dtype=torch.bfloat16, device=s["q"].device)
+        kvq.paged_decode_attn_combined(s["cpool"], 0, s["q"], s["table"], s["plan"], s["info"], s["work"], out)
+        return out
+    out = torch.empty(s["q"].shape, dtype=torch.bfloat16, device=s["q"].device)
+    kvq.paged_prefill_attn_fp8b(s["cpool"], 0, s["q"], s["table"], s["plan"], s["info"], s["work"], out)
+    return out
+
+
+def _cache(s):
+    """The pool as what its bytes are: E4M3 codes, and the scales."""
+    return s["pool"][:, :, :CODES].view(torch.float8_e4m3fn), s["pool"][:, :, CODES:CODES + 32].view(torch.float32)
+
+
+def _rotate(x, pos, cs, rot, inter):
+    """x [rows, heads, 256] fp32, rotated at its rows' positions."""
+    if rot == 0:
+        return x
+    c, n = cs[pos][:, None, :rot // 2], cs[pos][:, None, rot // 2:]
+    if inter:
+        a, b = x[..., 0:rot:2], x[..., 1:rot:2]
+        y = torch.stack([a * c - b * n, b * c + a * n], -1).flatten(-2)
+    else:
+        a, b = x[..., :rot // 2], x[..., rot // 2:rot]
+        y = torch.cat([a * c - b * n, b * c + a * n], -1)
+    return torch.cat([y, x[..., rot:]], -1)
+
+
+def _append(s):
+    dev, hkv, pool = s["pool"].device, s["hkv"], s["pool"]
+    rows, n_seq = s["k"].shape[0], len(s["lens"])
+    seq = torch.repeat_interleave(torch.arange(n_seq, device=dev), s["toks_dev"].long(), output_size=rows)
+    pos = torch.arange(rows, device=dev) - s["start"][seq] + s["pos0_dev"][seq]
+    k = _rotate(s["k"].float(), pos, s["table_cs"], s["rot"], s["inter"])
+    q = _rotate(s["q"].float(), pos, s["table_cs"], s["rot"], s["inter"])
+    # the tiles that get new tokens
+    per_seq = s["table"].shape[1] * 4
+    tile, at = torch.unique(seq * per_seq + pos // TILE, return_inverse=True)
+    owner, blk = tile // per_seq, tile % per_seq
+    slot, sub = s["table"][owner, blk // 4].long(), blk % 4
+    first = (s["pos0_dev"][owner] - blk * TILE).clamp(min=0)              # the tile's first new token
+    tiles = pool[:, :, :CODES].unflatten(-1, (4, TILE_BYTES))[slot, :, sub]
+    scale = pool[:, :, CODES:CODES + 32].view(torch.float32).unflatten(-1, (4, 2))[slot, :, sub]
+    new = torch.zeros((len(tile), TILE), dtype=torch.bool, device=dev)
+    new[at, pos % TILE] = True
+    old = torch.arange(TILE, device=dev)[None] < first[:, None]
+    new, old = new[:, None, :, None], old[:, None, :, None]
+    codes, scales = [], []
+    kv_codes = _unpack(tiles)
+    kv_rows = (k, s["v"].float())
+    for was, x, d0 in ((kv_codes[0], kv_rows[0], scale[..., 0]), (kv_codes[1], kv_rows[1], scale[..., 1])):
+        fill = torch.zeros((len(tile), hkv, TILE, D), device=dev)
+        fill[at, :, pos % TILE] = x
+        d0 = torch.where(first[:, None] > 0, d0, torch.zeros_like(d0))
+        d = torch.maximum(d0, _pow2(fill.abs().amax((2, 3))))
+        moved = _encode(was.view(torch.float8_e4m3fn).float() * d0[..., None, None], d[..., None, None])
+        codes.append(torch.where(new, _encode(fill, d[..., None, None]), torch.where(old, moved, was)))
+        scales.append(d)
+    s["pool"][:, :, :CODES].unflatten(-1, (4, TILE_BYTES))[slot, :, sub] = _pack(*codes)
+    s["pool"][:, :, CODES:CODES + 32].view(torch.float32).unflatten(-1, (4, 2))[slot, :, sub] = torch.stack(scales, -1)
+    return _cache(s), q.to(s["q_dtype"])
+
+
+def _gather(s):
+    """K and V values, fp32 [n_seq, hkv, max_len, 256], through the page table."""
+    table = s["table"].long().clamp(min=0)
+    pages = s["pool"][table]                                             # [n_seq, pages, hkv, bytes]
+    k, v = _unpack(pages[..., :CODES].unflatten(-1, (4, TILE_BYTES)))    # [n_seq, pages, hkv, 4, 64, 256]
+    scale = pages[..., CODES:CODES + 32].contiguous().view(torch.float32).unflatten(-1, (4, 2))
+    k = k.view(torch.float8_e4m3fn).float() * scale[..., 0, None, None]
+    v = v.view(torch.float8_e4m3fn).float() * scale[..., 1, None, None]
+    return k.transpose(1, 2).flatten(2, 4), v.transpose(1, 2).flatten(2, 4)
+
+
+def _decode(s):
+    k, v = _gather(s)
+    n, hkv, g = len(s["lens"]), s["hkv"], s["hq"] // s["hkv"]
+    sc = s["q"].reshape(n, hkv, g, D) @ k.transpose(2, 3) / 16
+    sc.masked_fill_(torch.arange(k.shape[2], device=k.device) >= s["lens_dev"][:, None, None, None], -math.inf)
+    p = torch.exp(sc - sc.amax(-1, keepdim=True))
+    return ((p @ v) / p.sum(-1, keepdim=True)).reshape(n, s["hq"], D).to(torch.bfloat16)
+
+
+def _prefill(s):
+    k, v = _gather(s)
+    n, hkv, g, top = len(s["lens"]), s["hkv"], s["hq"] // s["hkv"], max(s["toks"])
+    rows = s["q"].shape[0]
+    seq = torch.repeat_interleave(torch.arange(n, device=k.device), s["toks_dev"].long(), output_size=rows)
+    i = torch.arange(rows, device=k.device) - s["start"][seq]
+    q = torch.zeros((n, top, s["hq"], D), device=k.device)
+    q[seq, i] = s["q"].float()
+    q = q.reshape(n, top, hkv, g, D).permute(0, 2, 3, 1, 4).reshape(n, hkv, g * top, D)
+    sc = (q @ k.transpose(2, 3) / 16).reshape(n, hkv, g, top, -1)
+    limit = s["pos0_dev"][:, None] + torch.arange(top, device=k.device)[None]
+    sc.masked_fill_(torch.arange(k.shape[2], device=k.device) > limit[:, None, None, :, None], -math.inf)
+    sc.sub_(sc.amax(-1, keepdim=True)).exp_()
+    o = (sc.reshape(n, hkv, g * top, -1) @ v).reshape(n, hkv, g, top, D) / sc.sum(-1, keepdim=True)
+    return o.permute(0, 3, 1, 2, 4).reshape(n, top, s["hq"], D)[seq, i].to(torch.bfloat16)
+
+
+# ---- the definition in 64 bits --------------------------------------------------------------------------------------
+def exact(case, seed):
+    s = prepare(case, seed)
+    dev, hkv, g = s["pool"].device, s["hkv"], s["hq"] // s["hkv"]
+    t, d = torch.arange(TILE, device=dev)[:, None], torch.arange(D, device=dev)[None]
+    at_k = (d >> 7) * 8192 + (t >> 3) * 1024 + (t & 7) * 128 + ((((d >> 4) & 7) ^ (t & 7)) << 4) + (d & 15)
+    at_v = 16384 + (d >> 3) * 512 + (d & 7) * 64 + (((t >> 4) ^ ((d >> 1) & 3)) << 4) + (t & 15)
+    byte = torch.arange(256, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn).double()
+
+    def sequence(b, n, head):
+        """K and V of the first n tokens of sequence b."""
+        page = s["pool"][s["table"][b, :(n + PAGE - 1) // PAGE].long(), head]
+        sc = page[:, CODES:CODES + 32].contiguous().view(torch.float32).double().reshape(-1, 2)
+        tiles = page[:, :CODES].reshape(-1, TILE_BYTES)
+        return [(byte[tiles[:, at].long()] * sc[:, x, None, None]).reshape(-1, D)[:n] for x, at in ((0, at_k), (1, at_v))]
+
+    if case["op"] == "append":
+        half, codes, scales = s["rot"] // 2, s["pool"][:, :, :CODES].clone(), s["pool"][:, :, CODES:CODES + 32].clone().view(torch.float32)
+
+        def turned(x, pos):
+            x = x.double().clone()
+            c, n = s["table_cs"].double()[pos][:, None].split([half, half], -1) if half else (0, 0)
+            ia = torch.arange(half, device=dev) * 2 if s["inter"] else torch.arange(half, device=dev)
+            ib = ia + (1 if s["inter"] else half)
+            a, b = x[..., ia], x[..., ib]
+            x[..., ia], x[..., ib] = a * c - b * n, b * c + a * n
+            return x
+
+        table, grid = s["table"].tolist(), torch.sort(byte[byte.isfinite()])[0].unique()
+        values = byte[codes.long()] if codes.numel() < 3e8 else None
+        if values is None:
+            return None
+        qs, row = [], 0
+        for b, (p0, n) in enumerate(zip(s["pos0"], s["toks"])):
+            pos = torch.arange(p0, p0 + n, device=dev)
+            qs.append(turned(s["q"][row:row + n], pos))
+            new = (turned(s["k"][row:row + n], pos), s["v"][row:row + n].double())
+            for blk in range(p0 // TILE, (p0 + n - 1) // TILE + 1):
+                lo, hi = max(p0, blk * TILE), min(p0 + n, (blk + 1) * TILE)
+                slot, sub, t0 = table[b][blk // 4], blk % 4, lo - blk * TILE
+                for x, where in ((0, at_k), (1, at_v)):
+                    add = new[x][lo - p0:hi - p0].transpose(0, 1)                  # [hkv, tokens, 256]
+                    top = add.abs().amax((1, 2))
+                    d1 = torch.where(top > 0, torch.exp2(torch.ceil(torch.log2(top / 448))), torch.zeros_like(top))
+                    d0 = scales[slot, :, 2 * sub + x].double() * (t0 > 0)
+                    dn = torch.maximum(d0, d1)
+                    safe = torch.where(dn > 0, dn, torch.ones_like(dn))[:, None, None]
+                    scales[slot, :, 2 * sub + x] = dn.float()
+                    place = sub * TILE_BYTES + where
+                    old = values[slot][:, place[:t0]] * (d0[:, None, None] / safe)
+                    both = torch.cat([old, add / safe], 1)
+                    up = torch.searchsorted(grid, both.clamp(-448, 448).contiguous()).clamp(1, len(grid) - 1)
+                    lo_v, hi_v = grid[up - 1], grid[up]
+                    near = torch.where((both - lo_v) < (hi_v - both), lo_v, hi_v)   # a tie goes to the even code
+                    tie = (both - lo_v) == (hi_v - both)
+                    if bool(tie.any()):
+                        even = (lo_v.float().to(torch.float8_e4m3fn).view(torch.uint8) & 1) == 0
+                        near = torch.where(tie, torch.where(even, lo_v, hi_v), near)
+                    part = values[slot]
+                    part[:, place[:t0 + hi - lo]] = near
+                    values[slot] = part
+            row += n
+        return (values, scales), torch.cat(qs)
+    if case["op"] == "decode":
+        out = []
+        for b, n in enumerate(s["lens"]):
+            for h in range(hkv):
+                k, v = sequence(b, n, h)
+                p = torch.softmax(s["q"][b, h * g:(h + 1) * g].double() @ k.T / 16, -1)
+                out.append(p @ v)
+        return torch.cat(out).reshape(len(s["lens"]), s["hq"], D)
+    out, row = torch.empty(s["q"].shape, dtype=torch.float64, device=dev), 0
+    for b, (p0, n) in enumerate(zip(s["pos0"], s["toks"])):
+        for h in range(hkv):
+            k, v = sequence(b, p0 + n, h)
+            for i in range(0, n, 1024):
+                j = min(n, i + 1024)
+                x = s["q"][row + i:row + j, h * g:(h + 1) * g].double() @ k[:p0 + j].T / 16
+                hide = torch.arange(p0 + j, device=dev)[None] > torch.arange(p0 + i, p0 + j, device=dev)[:, None]
+                out[row + i:row + j, h * g:(h + 1) * g] = torch.softmax(x.masked_fill(hide[:, None], -math.inf), -1) @ v[:p0 + j]
+        row += n
+    return out
