@@ -63,16 +63,16 @@ def draw(rng):
     op = rng.choice(["append", "decode", "prefill"])
     hq, hkv = rng.choice([(24, 4), (16, 2), (4, 1), (12, 2), (8, 8), (7, 1), (10, 5)])
     if op == "append":
-        n = _log(rng, 1, 64)
-        toks, left = [], 8900
+        n, dtype, qf32 = _log(rng, 1, 64), rng.choice(["bf16", "f16", "f32"]), rng.random() < 0.5
+        e = 4 if dtype == "f32" else 2
+        toks, left = [], 270000000 // (D * (hq * (e + (4 if qf32 else e)) + 2 * hkv * (e + 1)))
         for _ in range(n):
-            t = min(_log(rng, 1, 6000) if rng.random() < 0.5 else 1, left - (n - len(toks)))
+            t = min(_log(rng, 1, 9000) if rng.random() < 0.5 else 1, left - (n - len(toks)))
             toks.append(max(t, 1))
             left -= toks[-1]
         pos0 = [rng.choice([0, _log(rng, 1, 30000)]) for _ in range(n)]
         return dict(op=op, hq=hq, hkv=hkv, pos0=",".join(map(str, pos0)), toks=",".join(map(str, toks)),
-                    dtype=rng.choice(["bf16", "f16", "f32"]), rot=rng.choice([0, 64, 128, 192, 256]),
-                    inter=rng.random() < 0.5, qf32=rng.random() < 0.5)
+                    dtype=dtype, rot=rng.choice([0, 64, 128, 192, 256]), inter=rng.random() < 0.5, qf32=qf32)
     if op == "decode":
         n = _log(rng, 1, 64)
         lens, left = [], 2100000 // hkv
