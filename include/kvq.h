@@ -12,6 +12,11 @@
  *   paged_decode_step_{int8,q4_0,k8v4,fp8,nvfp4}
  *                                 all of the above for one layer in one launch
  *   paged_prefill_attn            causal attention of a prompt chunk over the cache
+ *   kv_append_rope                kv_append of a ragged batch with the position
+ *                                 rotation of K and Q applied on the way
+ *   paged_decode_attn_fp8b, paged_prefill_attn_fp8b
+ *                                 attention over a cache in 8 bits with one scale
+ *                                 per block of 64 tokens and head
  *   kvq_resident_*                KV kept in pinned host memory behind a device
  *                                 page cache (residency table, CLOCK eviction)
  *
@@ -65,6 +70,7 @@ extern "C" {
 #define KVQ_STATUS_BAD_SLOT 1u   /* page-table entry outside [0, n_pages) */
 #define KVQ_STATUS_BAD_PLAN 2u   /* plan entry inconsistent with the pool */
 #define KVQ_STATUS_TIMEOUT 4u    /* a pipeline wait exceeded its time limit */
+#define KVQ_STATUS_NONFINITE 8u  /* fp8b append: a NaN (stored as 0) or an infinity (stored as the largest code) */
 
 #define KVQ_HEAD_DIM 256
 #define KVQ_PAGE_TOKENS 256
@@ -81,8 +87,22 @@ extern "C" {
  *            even, saturating); no rotation.
  *  KVQ_NVFP4 K and V as FP4 E2M1 codes with one E4M3 scale per 16 values,
  *            s = E4M3(max|x| / 6), code = E2M1(x / s) (round to nearest even,
- *            saturating); no per-tensor scale; no rotation. */
-typedef enum { KVQ_INT8 = 0, KVQ_Q4_0 = 1, KVQ_K8V4 = 2, KVQ_FP8 = 3, KVQ_NVFP4 = 4 } kvq_format;
+ *            saturating); no per-tensor scale; no rotation.
+ *  KVQ_FP8B  K and V as FP8 E4M3 codes with one fp32 scale for K and one for V
+ *            per tile of 64 tokens of one KV head (tokens 64 i .. 64 i + 63 of a
+ *            page); no rotation by H.  The scale d is the smallest power of two
+ *            with max|x| <= 448 d over the tile's values so far (0 when they are
+ *            all 0; exponent within -120 .. 118), code = E4M3(x / d) (round to
+ *            nearest even, saturating).  When an append raises a tile's scale, the
+ *            codes already there become E4M3(code d_old / d_new), exact unless the
+ *            result is a subnormal code.  The pages have no such format.  It is
+ *            written by kv_append_rope and read by the *_fp8b entry points;
+ *            kv_append, kv_append_q_rotate, paged_prefill_attn and
+ *            paged_decode_attn_cudacore return KVQ_EUNSUPPORTED for it. */
+typedef enum { KVQ_INT8 = 0, KVQ_Q4_0 = 1, KVQ_K8V4 = 2, KVQ_FP8 = 3, KVQ_NVFP4 = 4, KVQ_FP8B = 8 } kvq_format;
+
+/* Element types of the entry points that take more than fp32. */
+typedef enum { KVQ_F32 = 0, KVQ_BF16 = 1, KVQ_F16 = 2 } kvq_dtype;
 
 typedef struct {
     int32_t n_layers;     /* layers stored in the pool */
@@ -104,7 +124,12 @@ typedef struct {
  * K scales, V codes and V scales of its 8 tokens (offsets below).  Inside a
  * tile, codes and scales are arranged in the register-fragment order of the
  * attention kernel; the exact element order is documented with the kernels and
- * reproduced by the tests' layout decoder. */
+ * reproduced by the tests' layout decoder.
+ * KVQ_FP8B: a tile is 64 tokens of codes, K then V; the fp32 scales of a page
+ * block's four tiles stand behind them, K and V of tile i at bytes 8 i and
+ * 8 i + 4 of the scales.  There k_scales_off and v_scales_off are offsets in the
+ * page block, of tile 0's scales, and bytes_per_token_head leaves the 128 bytes
+ * of scales and padding per 256 tokens out. */
 typedef struct {
     int64_t tile_bytes;      /* bytes of one 8-token tile */
     int64_t k_codes_off;     /* offsets of the four sections inside a tile */
@@ -376,6 +401,108 @@ int paged_prefill_attn(const kvq_pool *pool, int layer, const float *q, int seq,
  * tie), and the workspace bytes it needs (0 for 1).  Host only; no CUDA call. */
 int kvq_prefill_split(const kvq_pool_desc *desc, int pos0, int n_tok, int n_sms, int *n_split,
                       uint64_t *workspace_bytes);
+
+/* kv_append_rope: append the new rows of a ragged batch to one layer of the
+ * pool, K rotated by its position on the way, and rotate the query rows in the
+ * same launch.  Any pool format; where the format stores K rotated by H/16, so
+ * are K and Q after the position rotation, and V as in kv_append.
+ *  cos_sin   device fp32 [n_pos][rot_dim]: row p holds the cosines of the
+ *            rot_dim / 2 angles at position p, then their sines.  rot_dim is a
+ *            multiple of 16 from 0 to 256; the dims from rot_dim on are left as
+ *            they are.  rot_dim 0: no rotation (cos_sin may be NULL)
+ *  interleaved  0: pair i is the dims (i, i + rot_dim/2); 1: (2i, 2i + 1).  A
+ *            pair (a, b) becomes (a c - b s, b c + a s), each product and sum
+ *            rounded once in fp32
+ *  q, k, v   device, elements of type dtype: row r of k and v is n_kv_heads
+ *            vectors of 256 at element r * k_stride (v_stride), row r of q is
+ *            n_q_heads vectors at r * q_stride; the strides are in elements, 16
+ *            bytes or a multiple, not below the row's own length.  k and v may be
+ *            NULL together (rotate q only), or q (append only)
+ *  row_start device int32 [n_seq + 1]: sequence s owns the rows row_start[s] ..
+ *            row_start[s+1] - 1 (possibly none), at the positions pos0[s],
+ *            pos0[s] + 1, ...  Rows from row_start[n_seq] to n_rows - 1 are
+ *            padding: neither read into the cache nor written to q_out
+ *  pos0      device int32 [n_seq]: the sequence's length before the call
+ *  q_out     device [n_rows][n_q_heads][256], contiguous, of type q_dtype:
+ *            KVQ_F32, or dtype itself when the pool is fp8b.  May be q when the
+ *            types and strides agree
+ * For fp8b the tile a sequence's pos0 falls into must hold its earlier tokens as
+ * this call wrote them; the tile's first token (position a multiple of 64)
+ * starts a new scale.  Codes and scales are then bit-exact functions of the
+ * tile's content and the call's rows.  For the other formats the codes are those
+ * of kv_append for the rotated rows.
+ * A page slot or a position out of range (of the page table, or of the cos_sin
+ * table) sets KVQ_STATUS_BAD_SLOT and skips the rows concerned; a row_start that
+ * decreases or passes n_rows sets KVQ_STATUS_BAD_PLAN.  Two sequences of the
+ * batch must not append to the same page.  KVQ_EALIGN for a pointer or a row
+ * stride that is not a multiple of 16 bytes. */
+int kv_append_rope(const kvq_pool *pool, int layer, const float *cos_sin, int n_pos, int rot_dim, int interleaved,
+                   const void *q, const void *k, const void *v, int dtype, int64_t q_stride, int64_t k_stride,
+                   int64_t v_stride, int64_t n_rows, const int32_t *row_start, const int32_t *pos0,
+                   const int32_t *page_table, int max_pages, int n_seq, void *q_out, int q_dtype, int32_t *status,
+                   void *stream);
+
+/* paged_decode_attn_fp8b, paged_decode_attn_fp8b_combined: single-token
+ * attention over an fp8b pool; the same arguments, plan, workspace and results
+ * as the entry points of the other formats above.  The combined form merges the
+ * units in a second small launch on the same stream; it does not use the
+ * workspace's counters, so the workspace needs no initialisation.  Calls on the
+ * same workspace must not overlap on the GPU.  A group all of whose pages are
+ * out of range gets zeros. */
+int paged_decode_attn_fp8b(const kvq_pool *pool, int layer, const float *q, const int32_t *page_table, int max_pages,
+                           const int32_t *plan, const kvq_plan_info *info, float *workspace, uint64_t workspace_bytes,
+                           int32_t *status, void *stream);
+int paged_decode_attn_fp8b_combined(const kvq_pool *pool, int layer, const float *q, const int32_t *page_table,
+                                    int max_pages, const int32_t *plan, const kvq_plan_info *info, float *workspace,
+                                    uint64_t workspace_bytes, uint16_t *out_bf16, float *out_f32, int32_t *status,
+                                    void *stream);
+
+/* Plan of a ragged prefill (host only): sequence s brings n_tok[s] >= 0 new
+ * tokens at positions pos0[s] .., so its token i attends to the keys
+ * 0 .. pos0[s] + i.  The (token, query head) rows of each KV head are taken in
+ * tiles of 128, and the plan deals the tiles' key ranges, in steps of 128 keys, to
+ * n_ctas CTAs (0 = one per SM of the current device) as evenly as possible; a tile
+ * cut between CTAs is merged from partial results in the workspace.  pos0, n_tok:
+ * host int32 [n_seq], pos0[s] >= 0 and pos0[s] + n_tok[s] <= max_pages * 256.
+ * plan, plan_capacity, info: as for kvq_decode_plan (KVQ_ESIZE with
+ * info->plan_len set when the array is too small).  KVQ_EUNSUPPORTED for a
+ * descriptor that is not fp8b. */
+typedef struct {
+    int32_t n_units;        /* row tiles and parts of row tiles */
+    int32_t n_ctas;         /* CTAs of the launch (0 when there are no rows) */
+    int32_t n_merges;       /* row tiles cut into parts */
+    int32_t n_slots;        /* partial results */
+    int32_t n_seq;
+    int32_t n_rows;         /* sum of n_tok: the rows of q */
+    int32_t n_kv_heads;
+    int32_t group;
+    int32_t plan_len;       /* int32 entries of the plan */
+    int32_t reserved;
+    uint64_t workspace_bytes;
+} kvq_prefill_info;
+
+int kvq_prefill_plan(const kvq_pool_desc *desc, int n_seq, const int32_t *pos0, const int32_t *n_tok, int max_pages,
+                     int n_ctas, int32_t *plan, int plan_capacity, kvq_prefill_info *info);
+
+/* paged_prefill_attn_fp8b: causal attention of the new tokens of a ragged batch
+ * over an fp8b pool that already holds them (kv_append_rope).
+ *  q         device, elements of type q_dtype, [n_rows] rows of [n_q_heads][256]
+ *            at element r * q_stride, the sequences' rows one after another in
+ *            the plan's order.  Scores are q.k_hat/16.  Q enters the tensor cores
+ *            as a sum of E4M3 terms under one power of two per row: two terms for
+ *            bf16, which hold its 8 bits, three (12 bits) for fp16 and fp32
+ *  plan      device copy of the kvq_prefill_plan array; info its host info
+ *  workspace device, at least info->workspace_bytes (may be NULL when that is 0),
+ *            needs no initialisation; calls that share it must not overlap
+ *  out_bf16  device [n_rows][n_q_heads][256] bf16 (required); out_f32 the same in
+ *            fp32 (optional)
+ * A slot out of range sets KVQ_STATUS_BAD_SLOT and its tokens are skipped (a row
+ * left with no key gets zeros); a plan entry that does not fit the call sets
+ * KVQ_STATUS_BAD_PLAN and its rows are not written. */
+int paged_prefill_attn_fp8b(const kvq_pool *pool, int layer, const void *q, int q_dtype, int64_t q_stride,
+                            const int32_t *page_table, int max_pages, const int32_t *plan,
+                            const kvq_prefill_info *info, float *workspace, uint64_t workspace_bytes,
+                            uint16_t *out_bf16, float *out_f32, int32_t *status, void *stream);
 
 /* attn_combine: for each (sequence, query head), merge the partials of its
  * units with the log-sum-exp rule (M = max m_j, L = sum l_j 2^(m_j - M),

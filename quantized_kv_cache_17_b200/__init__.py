@@ -7,8 +7,9 @@ missing, importing the binding's functions raises ``KVQError`` at once: there
 is no fallback implementation.
 
 Names follow the C ABI in ``include/kvq.h``: ``q_rotate``, ``kv_append``,
-``paged_decode_attn_{int8,q4_0,k8v4,fp8,nvfp4}``, ``attn_combine`` plus the host
-helpers ``pool_bytes``, ``pool_layout`` and ``decode_plan``.
+``kv_append_rope``, ``paged_decode_attn_{int8,q4_0,k8v4,fp8,nvfp4,fp8b}``,
+``attn_combine``, ``paged_prefill_attn``, ``paged_prefill_attn_fp8b`` plus the host
+helpers ``pool_bytes``, ``pool_layout``, ``decode_plan`` and ``prefill_plan``.
 """
 from __future__ import annotations
 
@@ -22,12 +23,12 @@ import numpy as np
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libkvq.so")
 
-INT8, Q4_0, K8V4, FP8, NVFP4 = 0, 1, 2, 3, 4
-FORMATS = {"int8": INT8, "q4_0": Q4_0, "k8v4": K8V4, "fp8": FP8, "nvfp4": NVFP4}
+INT8, Q4_0, K8V4, FP8, NVFP4, FP8B = 0, 1, 2, 3, 4, 8
+FORMATS = {"int8": INT8, "q4_0": Q4_0, "k8v4": K8V4, "fp8": FP8, "nvfp4": NVFP4, "fp8b": FP8B}
 HEAD_DIM = 256
 PAGE_TOKENS = 256
 
-STATUS_BAD_SLOT, STATUS_BAD_PLAN, STATUS_TIMEOUT = 1, 2, 4
+STATUS_BAD_SLOT, STATUS_BAD_PLAN, STATUS_TIMEOUT, STATUS_NONFINITE = 1, 2, 4, 8
 ERRORS = {-1: "KVQ_EINVAL", -2: "KVQ_EUNSUPPORTED", -3: "KVQ_EALIGN", -4: "KVQ_ECUDA", -5: "KVQ_ESIZE"}
 
 # entry points declared in include/kvq.h
@@ -41,8 +42,11 @@ EXPORTS = ["kvq_version", "kvq_pool_bytes", "kvq_pool_layout", "q_rotate", "kv_a
            "paged_decode_step_int8", "paged_decode_step_q4_0", "paged_decode_step_k8v4",
            "paged_decode_step_fp8", "paged_decode_step_nvfp4", "paged_prefill_attn", "kvq_prefill_split",
            "kvq_resident_state_bytes", "kvq_resident_init", "kvq_resident_map", "kvq_resident_load",
-           "kvq_resident_query", "kvq_resident_stats"]
-_FMT_NAMES = ("int8", "q4_0", "k8v4", "fp8", "nvfp4")
+           "kvq_resident_query", "kvq_resident_stats",
+           "kv_append_rope", "paged_decode_attn_fp8b", "paged_decode_attn_fp8b_combined", "kvq_prefill_plan",
+           "paged_prefill_attn_fp8b"]
+_FMT_NAMES = ("int8", "q4_0", "k8v4", "fp8", "nvfp4")     # formats with a scale per token or finer
+_DECODE_NAMES = _FMT_NAMES + ("fp8b",)
 
 
 class KVQError(RuntimeError):
@@ -71,6 +75,12 @@ class PlanInfo(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_uint64)]
 
 
+class PrefillInfo(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("n_units", "n_ctas", "n_merges", "n_slots", "n_seq", "n_rows",
+                                              "n_kv_heads", "group", "plan_len", "reserved")] + \
+               [("workspace_bytes", ctypes.c_uint64)]
+
+
 _lib = None
 
 
@@ -90,7 +100,7 @@ def lib():
         L.kv_append_q_rotate.argtypes = [ctypes.POINTER(Pool), I32, P, P, I64, P, P, P, I32, I32, P, P, I64, P, P]
         L.kvq_decode_plan.argtypes = [ctypes.POINTER(PoolDesc), I32, P, I32, I32, P, I32, ctypes.POINTER(PlanInfo)]
         dec = [ctypes.POINTER(Pool), I32, P, P, I32, P, ctypes.POINTER(PlanInfo), P, ctypes.c_uint64, P, P]
-        for f in _FMT_NAMES:
+        for f in _DECODE_NAMES:
             getattr(L, "paged_decode_attn_" + f).argtypes = dec
             getattr(L, "paged_decode_attn_" + f + "_combined").argtypes = dec[:-2] + [P, P] + dec[-2:]
         L.paged_decode_attn_q4_0_noalloc.argtypes = dec[:7] + [P, P, P, P]
@@ -101,6 +111,11 @@ def lib():
         L.attn_combine.argtypes = [P, P, ctypes.POINTER(PlanInfo), I32, P, P, P]
         L.paged_prefill_attn.argtypes = [ctypes.POINTER(Pool), I32, P, I32, I32, I32, P, I32, I32, I32, P,
                                          ctypes.c_uint64, P, P, P, P]
+        L.kv_append_rope.argtypes = [ctypes.POINTER(Pool), I32, P, I32, I32, I32, P, P, P, I32, I64, I64, I64, I64, P, P, P,
+                                     I32, I32, P, I32, P, P]
+        L.kvq_prefill_plan.argtypes = [ctypes.POINTER(PoolDesc), I32, P, P, I32, I32, P, I32, ctypes.POINTER(PrefillInfo)]
+        L.paged_prefill_attn_fp8b.argtypes = [ctypes.POINTER(Pool), I32, P, I32, I64, P, I32, P,
+                                              ctypes.POINTER(PrefillInfo), P, ctypes.c_uint64, P, P, P, P]
         L.kvq_prefill_split.argtypes = [ctypes.POINTER(PoolDesc), I32, I32, I32, ctypes.POINTER(ctypes.c_int),
                                         ctypes.POINTER(ctypes.c_uint64)]
         L.kvq_resident_init.argtypes = [P, ctypes.c_uint64, ctypes.POINTER(Pool), ctypes.POINTER(Pool)]
@@ -217,7 +232,7 @@ def decode_plan(desc: PoolDesc, seq_lens: Sequence[int], max_pages: int, n_ctas:
     return plan, info
 
 
-_DECODE = {FORMATS[f]: "paged_decode_attn_" + f for f in _FMT_NAMES}
+_DECODE = {FORMATS[f]: "paged_decode_attn_" + f for f in _DECODE_NAMES}
 NOALLOC_WS_BYTES = 8 << 20
 
 
@@ -252,6 +267,8 @@ def paged_decode_step(pool: KVPool, layer: int, q, k_new, v_new, page_table, pla
     """One decode step of a layer in one launch: append every sequence's newest
     token (k_new, v_new [n_seq, n_kv_heads, 256] at position seq_len - 1),
     rotate the raw query q where the format does, decode and merge."""
+    if pool.fmt not in _STEP:
+        raise KVQError("paged_decode_step failed: KVQ_EUNSUPPORTED")
     cp = pool.c_pool()
     name = _STEP[pool.fmt]
     _check(getattr(lib(), name)(ctypes.byref(cp), layer, _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(page_table),
@@ -297,6 +314,112 @@ def paged_decode_attn_fp8(pool, layer, q, page_table, plan_dev, info, workspace,
 def paged_decode_attn_nvfp4(pool, layer, q, page_table, plan_dev, info, workspace, status=None, stream=None):
     assert pool.fmt == NVFP4
     paged_decode_attn(pool, layer, q, page_table, plan_dev, info, workspace, status, stream)
+
+
+def paged_decode_attn_fp8b(pool, layer, q, page_table, plan_dev, info, workspace, status=None, stream=None):
+    assert pool.fmt == FP8B
+    paged_decode_attn(pool, layer, q, page_table, plan_dev, info, workspace, status, stream)
+
+
+def _dtype(t, what: str) -> int:
+    """The kvq_dtype of a tensor's elements."""
+    import torch
+    try:
+        return {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}[t]
+    except KeyError:
+        raise KVQError(f"{what}: {t} is not float32, bfloat16 or float16") from None
+
+
+def _rows(t, heads: int, what: str) -> int:
+    """The row stride, in elements, of a [rows, heads, 256] tensor whose heads lie side by side in a row."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != HEAD_DIM or t.stride(2) != 1 or \
+            (heads > 1 and t.stride(1) != HEAD_DIM):
+        raise KVQError(f"{what}: want [rows, {heads}, {HEAD_DIM}] with contiguous rows, got {tuple(t.shape)} with "
+                       f"strides {tuple(t.stride())}")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * HEAD_DIM)
+
+
+def kv_append_rope(pool: KVPool, layer: int, k, v, row_start, pos0, page_table, cos_sin=None, interleaved=False, q=None,
+                   q_out=None, q_out_dtype=None, status=None, stream=None):
+    """Append the rows k, v ([n_rows, n_kv_heads, 256] fp32, bf16 or fp16; rows may be
+    strided) of a ragged batch, K rotated at its position by the table cos_sin
+    ([n_pos, rot_dim] fp32: cosines, then sines; None: no rotation), and rotate q
+    ([n_rows, n_q_heads, 256] of the same type) likewise.  Sequence s owns rows
+    row_start[s] .. row_start[s+1] - 1 at positions pos0[s] ..; row_start, pos0 and
+    page_table are device int32.  Returns the rotated q (q_out, or a new tensor of
+    type q_out_dtype: fp32, or q's own type for fp8b pools; by default fp32 except
+    that fp8b keeps q's type), None without q.  k and v may both be None."""
+    import torch
+    d = pool.desc
+    first = k if k is not None else q
+    if first is None or (k is None) != (v is None):
+        raise KVQError("kv_append_rope failed: KVQ_EINVAL (k and v, q, or all three)")
+    n_rows, dt = first.shape[0], _dtype(first.dtype, "kv_append_rope")
+    for t, what in ((k, "k"), (v, "v"), (q, "q")):
+        if t is not None and (t.dtype != first.dtype or t.shape[0] != n_rows or t.device != first.device):
+            raise KVQError(f"kv_append_rope: {what} differs from the other rows in type, number or device")
+    ks, vs = (0, 0) if k is None else (_rows(k, d.n_kv_heads, "k"), _rows(v, d.n_kv_heads, "v"))
+    qs = 0 if q is None else _rows(q, d.n_q_heads, "q")
+    n_seq, max_pages = page_table.shape
+    if row_start.numel() != n_seq + 1 or pos0.numel() != n_seq:
+        raise KVQError("kv_append_rope: row_start has n_seq + 1 entries and pos0 n_seq")
+    for t, what in ((row_start, "row_start"), (pos0, "pos0"), (page_table, "page_table")):
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise KVQError(f"kv_append_rope: {what} is not a contiguous int32 tensor")
+    n_pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
+    if cos_sin is not None and (cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous()):
+        raise KVQError("kv_append_rope: cos_sin is not a contiguous float32 tensor")
+    if q is None:
+        q_out = None
+    elif q_out is None:
+        if q_out_dtype is None:
+            q_out_dtype = q.dtype if pool.fmt == FP8B else torch.float32
+        q_out = torch.empty((n_rows, d.n_q_heads, HEAD_DIM), dtype=q_out_dtype, device=q.device)
+    elif tuple(q_out.shape) != tuple(q.shape) or not q_out.is_contiguous():
+        raise KVQError("kv_append_rope: q_out is contiguous and shaped as q")
+    cp = pool.c_pool()
+    _check(lib().kv_append_rope(ctypes.byref(cp), layer, _ptr(cos_sin), n_pos, rot, 1 if interleaved else 0, _ptr(q),
+                                _ptr(k), _ptr(v), dt, qs, ks, vs, n_rows, _ptr(row_start), _ptr(pos0),
+                                _ptr(page_table), max_pages, n_seq, _ptr(q_out),
+                                0 if q_out is None else _dtype(q_out.dtype, "kv_append_rope"), _ptr(status),
+                                _stream(stream)), "kv_append_rope")
+    return q_out
+
+
+def prefill_plan(desc: PoolDesc, pos0: Sequence[int], n_tok: Sequence[int], max_pages: int, n_ctas: int = 0):
+    """Host plan of a ragged prefill over an fp8b pool: returns (plan int32 numpy array, PrefillInfo)."""
+    p = np.ascontiguousarray(np.asarray(pos0, np.int32))
+    n = np.ascontiguousarray(np.asarray(n_tok, np.int32))
+    if p.ndim != 1 or p.shape != n.shape:
+        raise KVQError("prefill_plan: pos0 and n_tok are lists of the same length")
+    info = PrefillInfo()
+    args = (ctypes.byref(desc), len(p), p.ctypes.data, n.ctypes.data, max_pages, n_ctas)
+    rc = lib().kvq_prefill_plan(*args, None, 0, ctypes.byref(info))
+    if rc != -5:
+        _check(rc, "kvq_prefill_plan")
+    plan = np.zeros(info.plan_len, np.int32)
+    _check(lib().kvq_prefill_plan(*args, plan.ctypes.data, len(plan), ctypes.byref(info)), "kvq_prefill_plan")
+    return plan, info
+
+
+def paged_prefill_attn_fp8b(pool: KVPool, layer: int, q, page_table, plan_dev, info: PrefillInfo, workspace, out_bf16,
+                            out_f32=None, status=None, stream=None):
+    """Causal attention of a ragged batch's new tokens over an fp8b pool that holds
+    them already: q [n_rows, n_q_heads, 256] (fp32, bf16 or fp16; rows may be
+    strided), rotated as the keys are; plan_dev a device copy of prefill_plan's
+    array; workspace None when info.workspace_bytes is 0."""
+    if q.shape[0] < info.n_rows:
+        raise KVQError("paged_prefill_attn_fp8b: q has fewer rows than the plan")
+    for t in (out_bf16, out_f32):
+        if t is not None and (tuple(t.shape[1:]) != tuple(q.shape[1:]) or t.shape[0] < info.n_rows or
+                              not t.is_contiguous()):
+            raise KVQError("paged_prefill_attn_fp8b: an output is contiguous and shaped as q")
+    cp = pool.c_pool()
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().paged_prefill_attn_fp8b(ctypes.byref(cp), layer, _ptr(q), _dtype(q.dtype, "paged_prefill_attn_fp8b"),
+                                         _rows(q, pool.desc.n_q_heads, "q"), _ptr(page_table), page_table.shape[1],
+                                         _ptr(plan_dev), ctypes.byref(info), _ptr(workspace), ws_bytes, _ptr(out_bf16),
+                                         _ptr(out_f32), _ptr(status), _stream(stream)), "paged_prefill_attn_fp8b")
 
 
 def prefill_split(desc: PoolDesc, pos0: int, n_tok: int, n_sms: int = 0):

@@ -29,6 +29,9 @@ COMMON = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", 
 SOURCES = {
     "kvq_abi.cu": [],
     "kvq_append.cu": ["-fmad=false"],     # quantiser: no fused multiply-add anywhere in this unit
+    "kvq_rope.cu": ["-fmad=false"],       # likewise
+    "kvq_block_decode.cu": [],
+    "kvq_block_prefill.cu": [],
     "kvq_decode.cu": [],
     "kvq_noalloc.cu": [],
     "kvq_resident.cu": [],

@@ -4,7 +4,7 @@
 #include <cstring>
 #include <vector>
 
-#include "kvq_internal.cuh"
+#include "kvq_block.cuh"
 
 using namespace kvq;
 
@@ -29,17 +29,25 @@ int64_t tile_bytes_for(int fmt) {
 
 void fill_layout(const kvq_pool_desc *d, kvq_layout *L) {
     const int kp = host_part_k(d->fmt), vp = host_part_v(d->fmt);
-    L->tile_bytes = tile_bytes_for(d->fmt);
     L->k_codes_off = 0;
-    L->k_scales_off = part_code_bytes(kp);
-    L->v_codes_off = L->k_scales_off + part_scale_bytes(kp);
-    L->v_scales_off = L->v_codes_off + part_code_bytes(vp);
-    L->page_bytes = L->tile_bytes * TILES_PER_PAGE;
+    if (d->fmt == KVQ_FP8B) {
+        L->tile_bytes = BT_BYTES;
+        L->v_codes_off = BT_K_BYTES;
+        L->k_scales_off = B_SCALES_OFF;
+        L->v_scales_off = B_SCALES_OFF + 4;
+        L->page_bytes = B_PAGE_BYTES;
+    } else {
+        L->tile_bytes = tile_bytes_for(d->fmt);
+        L->k_scales_off = part_code_bytes(kp);
+        L->v_codes_off = L->k_scales_off + part_scale_bytes(kp);
+        L->v_scales_off = L->v_codes_off + part_code_bytes(vp);
+        L->page_bytes = L->tile_bytes * TILES_PER_PAGE;
+    }
     L->head_stride = L->page_bytes;
     L->slot_stride = (int64_t)d->n_kv_heads * L->page_bytes;
     L->layer_stride = (int64_t)d->n_pages * L->slot_stride;
     L->total_bytes = (int64_t)d->n_layers * L->layer_stride;
-    L->bytes_per_token_head = L->tile_bytes / TILE;
+    L->bytes_per_token_head = L->tile_bytes / (d->fmt == KVQ_FP8B ? BT : TILE);
 }
 
 int check_pool(const kvq_pool *pool, int layer, PoolGeom *geo) {
@@ -57,6 +65,11 @@ int check_pool(const kvq_pool *pool, int layer, PoolGeom *geo) {
     geo->n_kv_heads = pool->desc.n_kv_heads;
     return KVQ_OK;
 }
+
+// Prefill plan: what a row tile costs beyond its steps of 128 keys, in steps, and
+// the shortest part worth a partial result (its merge moves as many bytes as four
+// steps read).
+constexpr int64_t PFB_TILE_COST = 3, PFB_MIN_PART = 4;
 
 int cuda_rc(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ECUDA; }
 
@@ -96,6 +109,10 @@ int decode_common(int fmt, bool tc, const kvq_pool *pool, int layer, const float
     const int rc = check_decode_args(fmt, pool, layer, q, page_table, max_pages, plan, info, workspace_bytes,
                                      out_bf16, out_f32, &geo);
     if (rc) return rc;
+    if (fmt == KVQ_FP8B)
+        return cuda_rc(launch_block_decode(static_cast<const uint8_t *>(pool->base), geo, layer, q, page_table, max_pages,
+                                           plan, *info, workspace, status, out_bf16, out_f32,
+                                           static_cast<cudaStream_t>(stream)));
     const int inverse = host_rotated_v(fmt) ? 1 : 0;
     return cuda_rc(launch_decode(fmt, tc, static_cast<const uint8_t *>(pool->base), geo, layer, q, page_table,
                                  max_pages, plan, *info, workspace, status, inverse, out_bf16, out_f32,
@@ -141,6 +158,7 @@ int kv_append(const kvq_pool *pool, int layer, const float *k, const float *v, i
     PoolGeom geo;
     int rc = check_pool(pool, layer, &geo);
     if (rc) return rc;
+    if (pool->desc.fmt == KVQ_FP8B) return KVQ_EUNSUPPORTED;   // rows in any order cannot share a tile's scale
     if (n_rows < 0 || max_pages <= 0 || n_seq <= 0) return KVQ_EINVAL;
     if (n_rows == 0) return KVQ_OK;
     if (!k || !v || !row_pos || !page_table) return KVQ_EINVAL;
@@ -157,6 +175,7 @@ int kv_append_q_rotate(const kvq_pool *pool, int layer, const float *k, const fl
     PoolGeom geo;
     int rc = check_pool(pool, layer, &geo);
     if (rc) return rc;
+    if (pool->desc.fmt == KVQ_FP8B) return KVQ_EUNSUPPORTED;
     if (n_rows < 0 || n_vec < 0 || max_pages <= 0 || n_seq <= 0) return KVQ_EINVAL;
     if (n_rows == 0 && n_vec == 0) return KVQ_OK;
     if (n_rows > 0 && (!k || !v || !row_pos || !page_table)) return KVQ_EINVAL;
@@ -277,11 +296,18 @@ int paged_decode_attn_nvfp4(const kvq_pool *pool, int layer, const float *q, con
                          workspace_bytes, status, stream);
 }
 
+int paged_decode_attn_fp8b(const kvq_pool *pool, int layer, const float *q, const int32_t *page_table, int max_pages,
+                           const int32_t *plan, const kvq_plan_info *info, float *workspace, uint64_t workspace_bytes,
+                           int32_t *status, void *stream) {
+    return decode_common(KVQ_FP8B, true, pool, layer, q, page_table, max_pages, plan, info, workspace,
+                         workspace_bytes, status, stream);
+}
+
 int paged_decode_attn_cudacore(int fmt, const kvq_pool *pool, int layer, const float *q, const int32_t *page_table,
                                int max_pages, const int32_t *plan, const kvq_plan_info *info, float *workspace,
                                uint64_t workspace_bytes, int32_t *status, void *stream) {
     if (!host_valid_format(fmt)) return KVQ_EINVAL;
-    if (fmt == KVQ_FP8 || fmt == KVQ_NVFP4) return KVQ_EUNSUPPORTED;   // the control covers the three 2-part formats
+    if (fmt == KVQ_FP8 || fmt == KVQ_NVFP4 || fmt == KVQ_FP8B) return KVQ_EUNSUPPORTED;   // the control covers the three 2-part formats
     if (pool) {
         const int G = pool->desc.n_kv_heads > 0 ? pool->desc.n_q_heads / pool->desc.n_kv_heads : 0;
         if (G != 4 && G != 6 && G != 8) return KVQ_EUNSUPPORTED;
@@ -303,6 +329,7 @@ KVQ_COMBINED(paged_decode_attn_q4_0_combined, KVQ_Q4_0)
 KVQ_COMBINED(paged_decode_attn_k8v4_combined, KVQ_K8V4)
 KVQ_COMBINED(paged_decode_attn_fp8_combined, KVQ_FP8)
 KVQ_COMBINED(paged_decode_attn_nvfp4_combined, KVQ_NVFP4)
+KVQ_COMBINED(paged_decode_attn_fp8b_combined, KVQ_FP8B)
 #undef KVQ_COMBINED
 
 #define KVQ_STEP(NAME, FMT)                                                                                     \
@@ -358,6 +385,7 @@ int paged_prefill_attn(const kvq_pool *pool, int layer, const float *q, int seq,
     PoolGeom geo;
     const int rc = check_pool(pool, layer, &geo);
     if (rc) return rc;
+    if (pool->desc.fmt == KVQ_FP8B) return KVQ_EUNSUPPORTED;   // paged_prefill_attn_fp8b
     if (!q || !page_table || !out_bf16 || n_tok <= 0 || pos0 < 0 || max_pages <= 0 || seq < 0 || seq >= n_seq)
         return KVQ_EINVAL;
     if ((int64_t)max_pages * PAGE > INT32_MAX || (int64_t)pos0 + n_tok > (int64_t)max_pages * PAGE) return KVQ_EINVAL;
@@ -377,6 +405,205 @@ int paged_prefill_attn(const kvq_pool *pool, int layer, const float *q, int seq,
                                   n_tok, page_table, max_pages, pool->desc.n_q_heads, n_split, split_tokens,
                                   workspace, host_rotated_v(pool->desc.fmt) ? 1 : 0, out_bf16, out_f32, status,
                                   static_cast<cudaStream_t>(stream)));
+}
+
+int kv_append_rope(const kvq_pool *pool, int layer, const float *cos_sin, int n_pos, int rot_dim, int interleaved,
+                   const void *q, const void *k, const void *v, int dtype, int64_t q_stride, int64_t k_stride,
+                   int64_t v_stride, int64_t n_rows, const int32_t *row_start, const int32_t *pos0,
+                   const int32_t *page_table, int max_pages, int n_seq, void *q_out, int q_dtype, int32_t *status,
+                   void *stream) {
+    PoolGeom geo;
+    const int rc = check_pool(pool, layer, &geo);
+    if (rc) return rc;
+    if (n_rows < 0 || n_seq <= 0 || max_pages <= 0 || (int64_t)max_pages * PAGE > INT32_MAX) return KVQ_EINVAL;
+    if (rot_dim < 0 || rot_dim > D || rot_dim % 16 != 0 || (interleaved != 0 && interleaved != 1)) return KVQ_EINVAL;
+    if (dtype < KVQ_F32 || dtype > KVQ_F16) return KVQ_EINVAL;
+    if (!k != !v || (!k && !q) || !q != !q_out) return KVQ_EINVAL;
+    if (q && q_dtype != KVQ_F32 && q_dtype != dtype) return KVQ_EINVAL;
+    if (q && q_dtype != KVQ_F32 && pool->desc.fmt != KVQ_FP8B) return KVQ_EUNSUPPORTED;   // those decodes take fp32
+    if (rot_dim && (!cos_sin || n_pos <= 0)) return KVQ_EINVAL;
+    const int n_q = pool->desc.n_q_heads;
+    // keeps the grid and the row arithmetic in range; row_start is int32
+    if (n_rows > (1 << 26) || n_seq > (1 << 24) || n_rows * n_q > ((int64_t)1 << 31) ||
+        (n_rows / 64 + 2 * (int64_t)n_seq) * geo.n_kv_heads + (n_rows * n_q + 15) / 16 > INT32_MAX)
+        return KVQ_EINVAL;
+    if ((k && (k_stride < (int64_t)geo.n_kv_heads * D || v_stride < (int64_t)geo.n_kv_heads * D)) ||
+        (q && q_stride < (int64_t)n_q * D))
+        return KVQ_EINVAL;
+    if (n_rows == 0) return KVQ_OK;
+    if (!row_start || !pos0 || !page_table) return KVQ_EINVAL;
+    const int64_t esize = dtype == KVQ_F32 ? 4 : 2;
+    if ((rot_dim && !aligned16(cos_sin)) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||
+        (k && (k_stride * esize % 16 || v_stride * esize % 16)) || (q && q_stride * esize % 16))
+        return KVQ_EALIGN;
+    RopeArgs R{layer, cos_sin, n_pos, rot_dim, interleaved, q, k, v, q_stride, k_stride, v_stride, n_rows,
+               row_start, pos0, page_table, max_pages, n_seq, n_q, q_out, status};
+    return cuda_rc(launch_rope_append(pool->desc.fmt, static_cast<uint8_t *>(pool->base), geo, R, dtype, q ? q_dtype : KVQ_F32,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+int kvq_prefill_plan(const kvq_pool_desc *desc, int n_seq, const int32_t *pos0, const int32_t *n_tok, int max_pages,
+                     int n_ctas, int32_t *plan, int plan_capacity, kvq_prefill_info *info) {
+    const int rc = check_desc(desc);
+    if (rc) return rc;
+    if (desc->fmt != KVQ_FP8B) return KVQ_EUNSUPPORTED;
+    if (n_seq <= 0 || !pos0 || !n_tok || !info || max_pages <= 0 || n_ctas < 0 || n_ctas > (1 << 16)) return KVQ_EINVAL;
+    if ((int64_t)max_pages * PAGE > INT32_MAX) return KVQ_EINVAL;
+    const int n_kv = desc->n_kv_heads, G = desc->n_q_heads / n_kv;
+    if (n_ctas == 0) {
+        int dev = 0, sms = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return KVQ_ECUDA;
+        n_ctas = sms;   // one prefill CTA per SM
+    }
+    // Work in steps of 128 keys; every row tile costs PFB_TILE_COST more, for its
+    // query and its output.
+    int64_t rows = 0, total = 0, tiles = 0;
+    for (int b = 0; b < n_seq; ++b) {
+        if (pos0[b] < 0 || n_tok[b] < 0 || (int64_t)pos0[b] + n_tok[b] > (int64_t)max_pages * PAGE) return KVQ_EINVAL;
+        rows += n_tok[b];
+    }
+    if (rows * G > INT32_MAX || rows * desc->n_q_heads > ((int64_t)1 << 31)) return KVQ_EUNSUPPORTED;
+    auto steps_of = [&](int b, int64_t r0) {
+        const int64_t last = std::min<int64_t>(n_tok[b], (r0 + PFB_ROWS - 1) / G + 1);   // tokens up to the tile's last
+        return (pos0[b] + last + PFB_KEYS - 1) / PFB_KEYS;
+    };
+    for (int b = 0; b < n_seq; ++b)
+        for (int64_t r0 = 0; r0 < (int64_t)n_tok[b] * G; r0 += PFB_ROWS) {
+            total += (steps_of(b, r0) + PFB_TILE_COST) * n_kv;
+            tiles += n_kv;
+        }
+    if (tiles > (1 << 24)) return KVQ_EUNSUPPORTED;
+    // Walk the row tiles in order and cut where a CTA's share is used up: the work
+    // that is left over the CTAs that are left, so that what one CTA takes too much
+    // or too little is spread over the later ones.  Parts shorter than PFB_MIN_PART
+    // steps are not made.
+    for (int pass = 0; pass < 2; ++pass) {
+        int64_t units = 0, merges = 0, slots = 0, cta = 0, used = 0, left = total, share = 0;
+        int32_t *U = nullptr, *M = nullptr, *S = nullptr;
+        if (pass == 1) {
+            U = plan + PLAN_HEADER;
+            M = U + (int64_t)info->n_units * PFB_UNIT;
+            S = M + (int64_t)info->n_merges * PFB_MERGE;
+            if (tiles) S[0] = 0;
+        }
+        auto open = [&]() {                // the next CTA's share
+            const int64_t ctas = std::max<int64_t>(n_ctas - cta, 1);
+            used = 0;
+            share = ctas == 1 ? INT64_MAX / 2 : std::max<int64_t>(PFB_MIN_PART + PFB_TILE_COST, (left + ctas - 1) / ctas);
+        };
+        auto close = [&]() {               // the current CTA ends here
+            ++cta;
+            if (pass == 1) S[cta] = (int32_t)units;
+            open();
+        };
+        open();
+        int64_t row_start = 0;
+        for (int b = 0; b < n_seq; ++b) {
+            for (int g = 0; g < n_kv; ++g)
+                for (int64_t r0 = 0; r0 < (int64_t)n_tok[b] * G; r0 += PFB_ROWS) {
+                    const int64_t steps = steps_of(b, r0);
+                    const int64_t keys = std::min<int64_t>(n_tok[b], (r0 + PFB_ROWS - 1) / G + 1) + pos0[b];
+                    int64_t s0 = 0, parts = 0;
+                    const int64_t slot0 = slots;
+                    while (s0 < steps) {
+                        const int64_t room = std::max<int64_t>(share - used - PFB_TILE_COST, 0), rest = steps - s0;
+                        int64_t n = rest;
+                        if (room < PFB_MIN_PART && used > 0) {     // nothing worth starting here
+                            close();
+                            continue;
+                        }
+                        if (rest > room + PFB_MIN_PART) n = room;
+                        const bool cut = n < rest || s0 > 0;
+                        if (pass == 1) {
+                            int32_t *u = U + units * PFB_UNIT;
+                            u[0] = b;
+                            u[1] = g;
+                            u[2] = (int32_t)r0;
+                            u[3] = (int32_t)(s0 * PFB_KEYS);
+                            u[4] = (int32_t)std::min<int64_t>((s0 + n) * PFB_KEYS, keys);
+                            u[5] = cut ? (int32_t)slots : -1;
+                            u[6] = (int32_t)row_start;
+                            u[7] = pos0[b];
+                            u[8] = n_tok[b];
+                            u[9] = u[10] = u[11] = 0;
+                        }
+                        ++units;
+                        if (cut) ++slots, ++parts;
+                        s0 += n;
+                        used += n + PFB_TILE_COST;
+                        left -= n + (s0 == steps ? PFB_TILE_COST : 0);
+                        if (used >= share) close();
+                    }
+                    if (parts) {
+                        if (pass == 1) {
+                            int32_t *m = M + merges * PFB_MERGE;
+                            m[0] = g;
+                            m[1] = (int32_t)r0;
+                            m[2] = (int32_t)slot0;
+                            m[3] = (int32_t)parts;
+                            m[4] = (int32_t)row_start;
+                            m[5] = n_tok[b];
+                            m[6] = m[7] = 0;
+                        }
+                        ++merges;
+                    }
+                }
+            row_start += n_tok[b];
+        }
+        if (used > 0) close();
+        if (pass == 0) {
+            const int64_t len = pfb_plan_len(units, merges, cta);
+            if (len > INT32_MAX) return KVQ_EUNSUPPORTED;
+            info->n_units = (int32_t)units;
+            info->n_ctas = (int32_t)cta;
+            info->n_merges = (int32_t)merges;
+            info->n_slots = (int32_t)slots;
+            info->n_seq = n_seq;
+            info->n_rows = (int32_t)rows;
+            info->n_kv_heads = n_kv;
+            info->group = G;
+            info->plan_len = (int32_t)len;
+            info->reserved = 0;
+            info->workspace_bytes = (uint64_t)slots * PFB_SLOT * sizeof(float);
+            if (!plan || plan_capacity < len) return KVQ_ESIZE;
+            const int32_t head[PLAN_HEADER] = {PFB_MAGIC, (int32_t)units, n_seq, (int32_t)rows, n_kv, G, (int32_t)merges,
+                                               (int32_t)cta};
+            std::copy(head, head + PLAN_HEADER, plan);
+            plan[len - 1] = 0;              // start[0] when there are no CTAs
+        }
+    }
+    return KVQ_OK;
+}
+
+int paged_prefill_attn_fp8b(const kvq_pool *pool, int layer, const void *q, int q_dtype, int64_t q_stride,
+                            const int32_t *page_table, int max_pages, const int32_t *plan,
+                            const kvq_prefill_info *info, float *workspace, uint64_t workspace_bytes,
+                            uint16_t *out_bf16, float *out_f32, int32_t *status, void *stream) {
+    PoolGeom geo;
+    const int rc = check_pool(pool, layer, &geo);
+    if (rc) return rc;
+    if (pool->desc.fmt != KVQ_FP8B) return KVQ_EINVAL;
+    if (!info || max_pages <= 0 || (int64_t)max_pages * PAGE > INT32_MAX) return KVQ_EINVAL;
+    const int n_q = pool->desc.n_q_heads;
+    if (info->group != n_q / geo.n_kv_heads || info->n_kv_heads != geo.n_kv_heads || info->n_seq <= 0 ||
+        info->n_units < 0 || info->n_ctas < 0 || info->n_merges < 0 || info->n_slots < 0 || info->n_rows < 0 ||
+        info->plan_len != pfb_plan_len(info->n_units, info->n_merges, info->n_ctas) ||
+        info->workspace_bytes != (uint64_t)info->n_slots * PFB_SLOT * sizeof(float))
+        return KVQ_EINVAL;
+    if (q_dtype < KVQ_F32 || q_dtype > KVQ_F16) return KVQ_EINVAL;
+    if (info->n_units == 0) return KVQ_OK;
+    if (!q || !page_table || !plan || !out_bf16 || q_stride < (int64_t)n_q * D || info->n_ctas == 0) return KVQ_EINVAL;
+    if (info->workspace_bytes > 0) {
+        if (!workspace) return KVQ_EINVAL;
+        if (workspace_bytes < info->workspace_bytes) return KVQ_ESIZE;
+    }
+    if (!aligned16(q) || !aligned16(plan) || !aligned16(workspace) || !aligned16(out_bf16) || !aligned16(out_f32) ||
+        q_stride * (q_dtype == KVQ_F32 ? 4 : 2) % 16)
+        return KVQ_EALIGN;
+    return cuda_rc(launch_block_prefill(static_cast<const uint8_t *>(pool->base), geo, layer, q, q_dtype, q_stride,
+                                        page_table, max_pages, plan, *info, workspace, status, out_bf16, out_f32,
+                                        static_cast<cudaStream_t>(stream)));
 }
 
 int attn_combine(const float *workspace, const int32_t *plan, const kvq_plan_info *info, int inverse_fwht,

@@ -112,7 +112,7 @@ inline int host_part_k(int fmt) {
 inline int host_part_v(int fmt) {
     return fmt == KVQ_INT8 ? PART_I8 : (fmt == KVQ_FP8 ? PART_F8 : (fmt == KVQ_NVFP4 ? PART_F4 : PART_Q4));
 }
-inline bool host_valid_format(int fmt) { return fmt >= KVQ_INT8 && fmt <= KVQ_NVFP4; }
+inline bool host_valid_format(int fmt) { return (fmt >= KVQ_INT8 && fmt <= KVQ_NVFP4) || fmt == KVQ_FP8B; }
 inline bool host_rotated_v(int fmt) { return fmt == KVQ_Q4_0 || fmt == KVQ_K8V4; }
 
 // ---------------------------------------------------------------------------
@@ -186,6 +186,24 @@ __host__ __device__ inline int ws_unit_floats(int G) { return G * D + WS_TAIL; }
 // (sequence, KV head) group (used by the fused combine), padded to 16 bytes.
 __host__ __device__ inline uint64_t ws_bytes_for(int n_units, int G, int n_groups) {
     return (uint64_t)n_units * ws_unit_floats(G) * 4 + (((uint64_t)n_groups * 4 + 15) & ~(uint64_t)15);
+}
+
+// ---------------------------------------------------------------------------
+// Prefill plan (int32): [magic, n_units, n_seq, n_rows, n_kv_heads, group, n_merges, n_ctas]
+//   units[n_units][12]  one row tile (128 of a sequence's (token, head) rows of one KV head, row i * group + h)
+//                       over the keys [k0, k1): {seq, kv_head, first row, k0, k1, partial slot or -1,
+//                       the sequence's first row of q, its pos0, its n_tok, 0, 0, 0}
+//   merges[n_merges][8] a row tile cut into parts: {kv_head, first row, first slot, parts, first row of q, n_tok, 0, 0}
+//   start[n_ctas + 1]   the units of each CTA
+// ---------------------------------------------------------------------------
+constexpr int PFB_MAGIC = 0x4B565150;   // "KVQP"
+constexpr int PFB_UNIT = 12, PFB_MERGE = 8;
+constexpr int PFB_ROWS = 128;           // rows of a row tile
+constexpr int PFB_KEYS = 128;           // keys of a step; cuts are multiples of it
+// floats of one partial: o[128][256], m[128], l[128]
+constexpr int PFB_SLOT = PFB_ROWS * (D + 2);
+inline int64_t pfb_plan_len(int64_t units, int64_t merges, int64_t ctas) {
+    return PLAN_HEADER + units * PFB_UNIT + merges * PFB_MERGE + ctas + 1;
 }
 
 // ---------------------------------------------------------------------------
@@ -347,6 +365,31 @@ cudaError_t launch_prefill(int fmt, const uint8_t *pool, const PoolGeom &geo, in
                            int pos0, int n_tok, const int32_t *page_table, int max_pages, int n_q_heads,
                            int n_split, int split_tokens, float *ws, int inverse_fwht, uint16_t *out_bf16,
                            float *out_f32, int32_t *status, cudaStream_t s);
+
+// A kv_append_rope call (see include/kvq.h for the meaning of each argument).
+struct RopeArgs {
+    int layer;
+    const float *cos_sin;
+    int n_pos, rot_dim, interleaved;
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride, n_rows;
+    const int32_t *row_start, *pos0, *page_table;
+    int max_pages, n_seq, n_q_heads;
+    void *q_out;
+    int32_t *status;
+};
+cudaError_t launch_rope_append(int fmt, uint8_t *pool, const PoolGeom &geo, const RopeArgs &R, int dtype, int q_dtype,
+                               cudaStream_t s);
+
+// Attention over an fp8b pool (kvq_block_decode.cu, kvq_block_prefill.cu).
+cudaError_t launch_block_decode(const uint8_t *pool, const PoolGeom &geo, int layer, const float *q,
+                                const int32_t *page_table, int max_pages, const int32_t *plan,
+                                const kvq_plan_info &info, float *ws, int32_t *status, uint16_t *out_bf16,
+                                float *out_f32, cudaStream_t s);
+cudaError_t launch_block_prefill(const uint8_t *pool, const PoolGeom &geo, int layer, const void *q, int q_dtype,
+                                 int64_t q_stride, const int32_t *page_table, int max_pages, const int32_t *plan,
+                                 const kvq_prefill_info &info, float *ws, int32_t *status, uint16_t *out_bf16,
+                                 float *out_f32, cudaStream_t s);
 
 // Split prefill: floats per (part, KV head, row) partial: o[256], m, l, padding.
 constexpr int PF_WS_STRIDE = 260;

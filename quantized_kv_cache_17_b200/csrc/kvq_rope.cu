@@ -1,0 +1,348 @@
+// kv_append_rope: new K and V rows of a ragged batch go into the paged cache with
+// the position rotation applied on the way, and the query rows are rotated in the
+// same launch.
+//
+// Rotation of a pair (a, b) with the table's c, s of its angle at the row's
+// position: (rn(rn(a c) - rn(b s)), rn(rn(b c) + rn(a s))), every operation a
+// single fp32 rounding (explicit intrinsics, no contraction), so the rotated row,
+// and with it the codes, are bit-exact functions of the input and the table.
+#include <cfloat>
+#include <type_traits>
+
+#include "kvq_append_dev.cuh"
+#include "kvq_block.cuh"
+
+namespace kvq {
+namespace {
+
+// Lane l's elements 8l .. 8l+7 of one row of 256.
+template <typename T> __device__ __forceinline__ void load_row8(const T *row, int lane, float (&x)[8]);
+template <> __device__ __forceinline__ void load_row8<float>(const float *row, int lane, float (&x)[8]) {
+    load8(row + lane * 8, x);
+}
+template <> __device__ __forceinline__ void load_row8<__nv_bfloat16>(const __nv_bfloat16 *row, int lane, float (&x)[8]) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(row) + lane);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+template <> __device__ __forceinline__ void load_row8<__half>(const __half *row, int lane, float (&x)[8]) {
+    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(row) + lane);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(u32_as_h2(w[i]));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
+__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __half) { return h2_as_u32(__floats2half2_rn(a, b)); }
+
+template <typename T> __device__ __forceinline__ void store_row8(T *row, int lane, const float (&x)[8]) {
+    if constexpr (sizeof(T) == 4) {
+        float4 *o = reinterpret_cast<float4 *>(row) + 2 * lane;
+        o[0] = make_float4(x[0], x[1], x[2], x[3]);
+        o[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+        reinterpret_cast<uint4 *>(row)[lane] = make_uint4(pack2(x[0], x[1], T{}), pack2(x[2], x[3], T{}),
+                                                          pack2(x[4], x[5], T{}), pack2(x[6], x[7], T{}));
+    }
+}
+
+// The warp rotates one row at table row cs (rot_dim floats: cosines, sines).
+// rot_dim is a multiple of 16, so a split pair's partner is the same element of
+// another lane, rot_dim / 16 lanes away.
+__device__ __forceinline__ void rope_row(float (&x)[8], const RopeArgs &R, const float *cs, int lane) {
+    const int half = R.rot_dim >> 1;
+    if (R.interleaved) {
+        const bool in = lane * 8 < R.rot_dim;
+        float4 c = make_float4(0.f, 0.f, 0.f, 0.f), s = c;
+        if (in) {
+            c = __ldg(reinterpret_cast<const float4 *>(cs) + lane);
+            s = __ldg(reinterpret_cast<const float4 *>(cs + half) + lane);
+        }
+        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+        if (in)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a = x[2 * i], b = x[2 * i + 1];
+                x[2 * i] = __fsub_rn(__fmul_rn(a, cc[i]), __fmul_rn(b, ss[i]));
+                x[2 * i + 1] = __fadd_rn(__fmul_rn(b, cc[i]), __fmul_rn(a, ss[i]));
+            }
+    } else {
+        const int hl = half >> 3;
+        const bool in = lane < 2 * hl, upper = lane >= hl;
+        const int src = in ? (upper ? lane - hl : lane + hl) : lane;
+        float c[8], s[8];
+        if (in) {
+            load8(cs + (upper ? lane - hl : lane) * 8, c);
+            load8(cs + half + (upper ? lane - hl : lane) * 8, s);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float o = __shfl_sync(0xffffffffu, x[i], src);
+            if (in)
+                x[i] = upper ? __fadd_rn(__fmul_rn(x[i], c[i]), __fmul_rn(o, s[i]))
+                             : __fsub_rn(__fmul_rn(x[i], c[i]), __fmul_rn(o, s[i]));
+        }
+    }
+}
+
+// Sequence and position of a row (by the whole warp).  False past the last
+// sequence's rows, and with a status bit where row_start or the position is bad.
+__device__ __forceinline__ bool row_place(const RopeArgs &R, int64_t row, int lane, int &seq, int &pos) {
+    if (row >= __ldg(R.row_start + R.n_seq)) return false;
+    seq = warp_find_last(R.n_seq, row, lane, [&](int s) { return (int64_t)__ldg(R.row_start + s); });
+    if (seq < 0 || row >= __ldg(R.row_start + seq + 1)) {
+        if (lane == 0) status_or(R.status, KVQ_STATUS_BAD_PLAN);
+        return false;
+    }
+    const int64_t p = (int64_t)__ldg(R.pos0 + seq) + (row - __ldg(R.row_start + seq));
+    if (p < 0 || p >= (int64_t)R.max_pages * PAGE || (R.rot_dim && p >= R.n_pos)) {
+        if (lane == 0) status_or(R.status, KVQ_STATUS_BAD_SLOT);
+        return false;
+    }
+    pos = (int)p;
+    return true;
+}
+
+// One query row of one head: rotate, rotate once more by H/16 where the format
+// keeps K that way, store.
+template <bool FWHT, typename T, typename TQ>
+__device__ __forceinline__ void rope_query(const RopeArgs &R, int64_t item, int lane) {
+    const int64_t row = item / R.n_q_heads;
+    const int head = (int)(item - row * R.n_q_heads);
+    if (row >= R.n_rows) return;
+    float x[8];
+    load_row8<T>(static_cast<const T *>(R.q) + row * R.q_stride + head * D, lane, x);
+    int seq, pos;
+    if (!row_place(R, row, lane, seq, pos)) return;
+    if (R.rot_dim) rope_row(x, R, R.cos_sin + (int64_t)pos * R.rot_dim, lane);
+    if (FWHT) fwht256_lane(x, lane);
+    store_row8<TQ>(static_cast<TQ *>(R.q_out) + (row * R.n_q_heads + head) * D, lane, x);
+}
+
+// Formats whose scales are a token's own: one warp per (row, KV head), then one
+// per (row, query head).
+template <int FMT, typename T>
+__global__ void __launch_bounds__(128) rope_append_kernel(uint8_t *pool, PoolGeom geo, RopeArgs R, unsigned kv_blocks) {
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31;
+    if (blockIdx.x >= kv_blocks) {
+        rope_query<Fmt<FMT>::KROT, T, float>(R, (int64_t)(blockIdx.x - kv_blocks) * 4 + (threadIdx.x >> 5), lane);
+        return;
+    }
+    const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int64_t row = item / geo.n_kv_heads;
+    const int head = (int)(item - row * geo.n_kv_heads);
+    if (row >= R.n_rows) return;
+    float xk[8], xv[8];
+    load_row8<T>(static_cast<const T *>(R.k) + row * R.k_stride + head * D, lane, xk);
+    load_row8<T>(static_cast<const T *>(R.v) + row * R.v_stride + head * D, lane, xv);
+    int seq, pos;
+    if (!row_place(R, row, lane, seq, pos)) return;
+    const int slot = __ldg(R.page_table + (int64_t)seq * R.max_pages + (pos >> 8));
+    uint8_t *tile = token_tile<FMT>(pool, geo, R.layer, slot, head, pos, R.status, lane);
+    if (!tile) return;
+    if (R.rot_dim) rope_row(xk, R, R.cos_sin + (int64_t)pos * R.rot_dim, lane);
+    TokenCodes t;
+    quant_token<FMT>(xk, xv, lane, t);
+    store_token<FMT>(t, lane, pos & 7, tile);
+}
+
+// ---- fp8b ------------------------------------------------------------------
+constexpr int BA_THREADS = 512;
+
+// 16 codes times the power of two f (0 clears them); bytes whose token is not
+// below keep (bit i of keep: byte i is an old token's) stay as they are.
+__device__ __forceinline__ uint4 rescale16(uint4 u, float f, uint32_t keep) {
+    uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t r = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float2 v = __half22float2(u32_as_h2(e4m3x2_to_h2((w[i] >> (16 * h)) & 0xFFFFu)));
+            r |= f32x2_to_e4m3x2(__fmul_rn(v.x, f), __fmul_rn(v.y, f)) << (16 * h);
+        }
+        uint32_t m = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) m |= (keep >> (4 * i + b) & 1u) ? 0xFFu << (8 * b) : 0u;
+        w[i] = (r & m) | (w[i] & ~m);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One CTA per (sequence, tile it appends to, KV head); the CTAs after those take
+// the query rows, one warp per (row, head).  Item i belongs to the sequence s
+// whose range [row_start[s] / 64 + 2 s, row_start[s+1] / 64 + 2 (s+1)) holds it:
+// n rows touch at most n / 64 + 2 tiles, so the ranges are found from row_start
+// alone and a surplus item has no rows.  Even warps hold K rows and odd warps V
+// rows, one row's 8 values a lane, up to 8 rows a warp, so the tile's rows are
+// read once and stay in registers between the scale and the codes.
+template <typename T, typename TQ>
+__global__ void __launch_bounds__(BA_THREADS, 1) block_append_kernel(uint8_t *pool, PoolGeom geo, RopeArgs R,
+                                                                     unsigned kv_blocks) {
+    __shared__ float s_max[BA_THREADS / 32];
+    __shared__ __align__(16) uint8_t s_v[32 * 528];     // V codes: 512 bytes a dim group, 16 of padding
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (blockIdx.x >= kv_blocks) {
+        rope_query<false, T, TQ>(R, (int64_t)(blockIdx.x - kv_blocks) * (BA_THREADS / 32) + warp, lane);
+        return;
+    }
+    const int64_t item = blockIdx.x / geo.n_kv_heads;
+    const int head = (int)(blockIdx.x - item * geo.n_kv_heads);
+    const int seq = warp_find_last(R.n_seq, item, lane, [&](int s) { return (int64_t)(__ldg(R.row_start + s) >> 6) + 2 * (int64_t)s; });
+    if (seq < 0) {
+        if (threadIdx.x == 0) status_or(R.status, KVQ_STATUS_BAD_PLAN);
+        return;
+    }
+    const int row0 = __ldg(R.row_start + seq), row1 = __ldg(R.row_start + seq + 1), p0 = __ldg(R.pos0 + seq);
+    if (row0 < 0 || row1 < row0 || row1 > R.n_rows) {
+        if (threadIdx.x == 0) status_or(R.status, KVQ_STATUS_BAD_PLAN);
+        return;
+    }
+    if (row1 == row0) return;
+    int64_t end = (int64_t)p0 + (row1 - row0);
+    const int64_t room = R.rot_dim ? min((int64_t)R.max_pages * PAGE, (int64_t)R.n_pos) : (int64_t)R.max_pages * PAGE;
+    if (p0 < 0 || end > room) {
+        if (threadIdx.x == 0) status_or(R.status, KVQ_STATUS_BAD_SLOT);
+        if (p0 < 0) return;
+        end = min(end, room);
+    }
+    const int64_t tile_i = (int64_t)(p0 >> 6) + (item - ((int64_t)(row0 >> 6) + 2 * (int64_t)seq));
+    const int64_t first = tile_i * BT;
+    if (first >= end) return;
+    const int t0 = first >= p0 ? 0 : (int)(p0 - first), t1 = (int)min((int64_t)BT, end - first);
+    const int slot = __ldg(R.page_table + (int64_t)seq * R.max_pages + (first >> 8));
+    if (slot < 0 || slot >= geo.n_pages) {
+        if (threadIdx.x == 0) status_or(R.status, KVQ_STATUS_BAD_SLOT);
+        return;
+    }
+    uint8_t *page = pool + R.layer * geo.layer_stride + (int64_t)slot * geo.slot_stride + (int64_t)head * geo.page_bytes;
+    uint8_t *tile = page + (tile_i & 3) * BT_BYTES;
+    float *scale = reinterpret_cast<float *>(page + B_SCALES_OFF) + 2 * (tile_i & 3);
+    const int64_t rbase = row0 + (first - p0);          // the row of the tile's token 0 (may lie before row0)
+    const bool is_v = warp & 1;
+    const float d0 = t0 > 0 ? scale[is_v] : 0.0f;
+
+    // rows: token 8 (warp / 2) + i of the tile, i = 0 .. 7
+    float x[8][8];
+    float amax = 0.0f;
+    bool odd_value = false;
+    const T *src = is_v ? static_cast<const T *>(R.v) : static_cast<const T *>(R.k);
+    const int64_t stride = is_v ? R.v_stride : R.k_stride;
+    const int tok0 = 8 * (warp >> 1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (tok0 + i >= t0 && tok0 + i < t1) load_row8<T>(src + (rbase + tok0 + i) * stride + head * D, lane, x[i]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (tok0 + i >= t0 && tok0 + i < t1) {
+            if (!is_v && R.rot_dim) rope_row(x[i], R, R.cos_sin + (first + tok0 + i) * R.rot_dim, lane);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (!(fabsf(x[i][e]) <= FLT_MAX)) {     // NaN is kept out of the cache, infinity saturates
+                    odd_value = true;
+                    x[i][e] = x[i][e] != x[i][e] ? 0.0f : copysignf(FLT_MAX, x[i][e]);
+                }
+                amax = fmaxf(amax, fabsf(x[i][e]));
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 16; m; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+    if (__any_sync(0xffffffffu, odd_value) && lane == 0) status_or(R.status, KVQ_STATUS_NONFINITE);
+    if (lane == 0) s_max[warp] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < BA_THREADS / 64; ++w) amax = fmaxf(amax, s_max[2 * w + is_v]);
+    const float d = fmaxf(d0, block_scale(amax));
+    if (warp < 2 && lane == 0) scale[is_v] = d;
+
+    const float f = d > 0.0f ? d0 / d : 1.0f;           // exact: both are powers of two (or d0 = 0)
+    const int wi = (warp >> 1) * 32 + lane;              // thread among the 256 of its side
+    const bool whole_v = t0 == 0 && t1 == BT;
+    if (!is_v) {
+        if (t0 > 0 && f != 1.0f)
+            for (int c = wi; c < t0 * 16; c += BA_THREADS / 2) {
+                uint4 *p = reinterpret_cast<uint4 *>(tile + block_k_off(c >> 4, (c & 15) * 16));
+                *p = rescale16(*p, f, 0xFFFFu);
+            }
+    } else if (!whole_v) {                               // the tile's bytes, rescaled, come to shared memory first
+        for (int c = wi; c < 1024; c += BA_THREADS / 2) {
+            uint4 u = *reinterpret_cast<const uint4 *>(tile + BT_K_BYTES + c * 16);
+            const int row = c >> 2, tok = ((c & 3) ^ ((row >> 1) & 3)) * 16;
+            if (t0 > tok && f != 1.0f) u = rescale16(u, f, t0 - tok >= 16 ? 0xFFFFu : (1u << (t0 - tok)) - 1u);
+            *reinterpret_cast<uint4 *>(s_v + (c >> 5) * 528 + (c & 31) * 16) = u;
+        }
+    }
+    __syncthreads();
+    const float inv = d > 0.0f ? 1.0f / d : 0.0f;        // a power of two: x * inv is x / d
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int t = tok0 + i;
+        if (t < t0 || t >= t1) continue;
+        uint32_t c[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            c[j] = f32x2_to_e4m3x2(__fmul_rn(x[i][2 * j], inv), __fmul_rn(x[i][2 * j + 1], inv));
+            if (!(d > 0.0f)) c[j] = 0;
+        }
+        if (!is_v) {
+            *reinterpret_cast<uint2 *>(tile + block_k_off(t, lane * 8)) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                s_v[lane * 528 + e * 64 + (((t >> 4) ^ ((e >> 1) & 3)) << 4) + (t & 15)] = (uint8_t)(c[e >> 1] >> (8 * (e & 1)));
+        }
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < 1024; c += BA_THREADS)
+        reinterpret_cast<uint4 *>(tile + BT_K_BYTES)[c] = *reinterpret_cast<const uint4 *>(s_v + (c >> 5) * 528 + (c & 31) * 16);
+}
+
+template <typename T, typename TQ>
+cudaError_t launch_typed(int fmt, uint8_t *pool, const PoolGeom &geo, const RopeArgs &R, cudaStream_t s) {
+    const int64_t q_items = R.q ? R.n_rows * R.n_q_heads : 0;
+    if (fmt == KVQ_FP8B) {
+        const int64_t kv = R.k ? ((R.n_rows >> 6) + 2 * (int64_t)R.n_seq) * geo.n_kv_heads : 0;
+        const int64_t qb = (q_items + BA_THREADS / 32 - 1) / (BA_THREADS / 32);
+        return launch_ex(block_append_kernel<T, TQ>, dim3((unsigned)(kv + qb)), dim3(BA_THREADS), 0, s, false, pool, geo,
+                         R, (unsigned)kv);
+    }
+    if constexpr (std::is_same_v<TQ, float>) {           // the decodes of these formats take fp32 queries
+        const int64_t kv = R.k ? (R.n_rows * geo.n_kv_heads + 3) / 4 : 0, qb = (q_items + 3) / 4;
+        auto kern = fmt == KVQ_INT8    ? rope_append_kernel<KVQ_INT8, T>
+                    : fmt == KVQ_Q4_0  ? rope_append_kernel<KVQ_Q4_0, T>
+                    : fmt == KVQ_K8V4  ? rope_append_kernel<KVQ_K8V4, T>
+                    : fmt == KVQ_FP8   ? rope_append_kernel<KVQ_FP8, T>
+                                       : rope_append_kernel<KVQ_NVFP4, T>;
+        return launch_ex(kern, dim3((unsigned)(kv + qb)), dim3(128), 0, s, false, pool, geo, R, (unsigned)kv);
+    } else {
+        return cudaErrorNotSupported;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_rope_append(int fmt, uint8_t *pool, const PoolGeom &geo, const RopeArgs &R, int dtype, int q_dtype,
+                               cudaStream_t s) {
+    if (dtype == KVQ_F32) return launch_typed<float, float>(fmt, pool, geo, R, s);
+    if (dtype == KVQ_BF16)
+        return q_dtype == KVQ_F32 ? launch_typed<__nv_bfloat16, float>(fmt, pool, geo, R, s)
+                                  : launch_typed<__nv_bfloat16, __nv_bfloat16>(fmt, pool, geo, R, s);
+    return q_dtype == KVQ_F32 ? launch_typed<__half, float>(fmt, pool, geo, R, s)
+                              : launch_typed<__half, __half>(fmt, pool, geo, R, s);
+}
+
+}  // namespace kvq
