@@ -98,8 +98,8 @@ __global__ void __launch_bounds__(BD_THREADS, 1) block_decode_kernel(BdArgs A) {
         const int32_t *row = A.page_table + (int64_t)seq * A.max_pages;
         const uint8_t *base = A.pool + A.layer * A.geo.layer_stride + (int64_t)kvh * A.geo.page_bytes;
         const int page0 = t0 >> 8, page_end = (t1 + PAGE - 1) >> 8;
-        int held = -1, held_from = page0 - 32;
-        for (int i = 0; i < n_tiles; ++i) {
+        int held = -1, held_from = page0 - 32, i = 0;
+        for (; i < n_tiles; ++i) {
             const int tile = (t0 >> 6) + i, page = tile >> 2, s = i % BD_STAGES, use = i / BD_STAGES;
             if (page >= held_from + 32) {          // 32 page-table entries at a time
                 held_from = page;
@@ -126,6 +126,8 @@ __global__ void __launch_bounds__(BD_THREADS, 1) block_decode_kernel(BdArgs A) {
             }
             __syncwarp();
         }
+        // no copy is left in flight
+        for (int o = max(0, i - BD_STAGES); o < i; ++o) mbar_wait_bounded(&T.full[o % BD_STAGES], (o / BD_STAGES) & 1, BD_WAIT_NS);
     } else {
         // ---- query: head `warp` to shared memory, then fragments ----
         {

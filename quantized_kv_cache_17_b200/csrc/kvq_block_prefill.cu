@@ -1,8 +1,11 @@
 // paged_prefill_attn_fp8b: causal attention of a ragged batch's new tokens over
 // the fp8b pool.
+#include <cfloat>
 #include <mutex>
+#include <type_traits>
 
 #include "kvq_block.cuh"
+#include "kvq_tcgen05.cuh"
 
 namespace kvq {
 namespace {
@@ -48,121 +51,502 @@ __device__ __forceinline__ bool plan_ok(const PfbArgs &A) {
     return ok;
 }
 
-__device__ __forceinline__ float load_q(const void *q, int dtype, int64_t i) {
-    if (dtype == KVQ_F32) return static_cast<const float *>(q)[i];
-    if (dtype == KVQ_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(q)[i]);
-    return __half2float(static_cast<const __half *>(q)[i]);
+// ---------------------------------------------------------------------------
+// The kernel: one CTA per SM, 320 threads, walking its units.
+//   warps 0-7  softmax.  Warp w and warp w + 4 share the 32 rows 32 (w % 4) ..; a
+//              thread has one row and 64 of a step's 128 keys, one 64-token tile
+//              and so one K and one V scale.
+//   warp 8     bulk copies of K and V codes into a ring of 32 KB slots, in the
+//              order the tensor core uses them: K0 K1 V0 K2 V1 ...
+//   warp 9     one lane issues every tcgen05.mma.
+// Both products take the codes as they lie in the pool (kind::f8f6f4, B operand):
+//   S[128 rows][128 keys] = sum over terms of Q_i K^T: a row of Q, scaled so that
+//     its largest value lies in [2^7, 2^8), is a sum of E4M3 terms, each the
+//     rounding of what the earlier ones leave.  Two terms hold bf16's 8 bits (4
+//     each) down to 2^-10, which is 2^-17 of the row's largest; three hold 12.
+//   O[128 rows][256 dims] += sum over three terms of W_i V: a weight as fp16 (11
+//     bits), then three E5M2 terms of 3 bits each: E5M2 is the upper byte of fp16,
+//     so a term is an integer rounding of the bits and what it leaves an exact fp16
+//     difference.  E5M2 and not E4M3, for range: weights from 2^15 down to 2^-16.
+// The five 8-bit passes cost 1.25 times two 16-bit ones; what they save is the
+// conversion of every K and V code to 16 bits, which would move as many bytes
+// through shared memory as the products themselves.
+// Weights: W = 2^(s - m) 2^(e_v - E) 2^12, with s the score in base 2, m the row's
+// reference, e_v the exponent of the tile's V scale and E the largest e_v of the
+// unit so far, so V scales cost nothing.  m moves only when a score passes it by
+// 2^3: then, or when E moves, the row's O is multiplied in TMEM.
+// TMEM, all 512 columns: O 0-255; S of even steps 256-383, of odd ones 384-511.
+// The weights of the 32 keys c overwrite their scores: term i at 32 c + 8 i.
+// Two products that touch the same S / P columns (the values of step j, the scores
+// of step j + 2) are ordered by a wait on the former's commit.
+// ---------------------------------------------------------------------------
+constexpr int PF_SOFT = 8;                       // softmax warps
+constexpr int PF_THREADS = (PF_SOFT + 2) * 32;
+constexpr int PF_SLOT_BYTES = 32768;
+constexpr uint64_t PF_WAIT_NS = 2000000000ull;
+constexpr int PF_S_COL = 256;
+constexpr int PF_NO_E = -10000;
+
+template <int TERMS> struct PfCfg {
+    static constexpr int SLOTS = TERMS == 2 ? 5 : 4;
+    static constexpr int Q_BYTES = TERMS * 32768;
+    static constexpr int RING = Q_BYTES;
+    static constexpr int TAIL = RING + SLOTS * PF_SLOT_BYTES;
+    static constexpr int SMEM = TAIL + 2048 + 1024;         // the tail; the ring starts on an atom's boundary
+};
+struct PfTail {
+    uint64_t full[5], empty[5], s_full[2], p_full[2], o_done, q_full, drained;
+    uint32_t tmem;
+    int abort;
+    float qscale[PFB_ROWS];
+    float red[2][PFB_ROWS];
+};
+static_assert(sizeof(PfTail) <= 2048, "tail");
+static_assert(PfCfg<2>::SMEM <= 232448 && PfCfg<3>::SMEM <= 232448, "227 KB a CTA");
+
+__device__ __forceinline__ float pow2f(int e) { return e < -126 ? 0.0f : __uint_as_float((uint32_t)(min(e, 127) + 127) << 23); }
+
+// The whole pair of warps (64 threads, barrier id) agrees on whether any thread asks.
+__device__ __forceinline__ bool pair_any(bool ask, int id) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, 64, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"((uint32_t)ask), "r"(id)
+                 : "memory");
+    return r != 0;
 }
 
-// One CTA per plan CTA; each warp takes four rows of a unit at a time, a lane two
-// keys of a 64-token tile for the scores and eight dims for the values, in fp32.
-constexpr int PS_WARPS = 8;
-__global__ void __launch_bounds__(PS_WARPS * 32) block_prefill_kernel(PfbArgs A, int q_dtype) {
-    __shared__ float qs[PS_WARPS][4][D];
-    __shared__ float ps[PS_WARPS][4][BT];
-    grid_dependency_wait();
-    if (!plan_ok(A)) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int32_t *start = A.plan + PLAN_HEADER + (int64_t)A.n_units * PFB_UNIT + (int64_t)A.n_merges * PFB_MERGE;
-    const int i0 = max(0, start[blockIdx.x]), i1 = min(A.n_units, start[blockIdx.x + 1]);
-    for (int i = i0; i < i1; ++i) {
-        Unit u;
-        if (!load_unit(A, i, u)) continue;
-        const int n_rows = u.n_tok * A.G;
-        for (int rr = warp * 4; rr < PFB_ROWS; rr += PS_WARPS * 4) {
-            const int r = u.r0 + rr;
-            if (r >= n_rows) break;
-            int limit[4];
-            float m[4], l[4], o[4][8];
-            __syncwarp();
+template <typename T> __device__ __forceinline__ void load_q8(const T *p, float (&x)[8]) {
+    if constexpr (sizeof(T) == 4) {
+        const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    } else {
+        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int ri = min(r + x, n_rows - 1), tok = ri / A.G, h = u.head * A.G + ri % A.G;
-                limit[x] = min(u.k1, u.pos0 + tok + 1);
-                m[x] = -INFINITY;
-                l[x] = 0.0f;
-                for (int d = lane; d < D; d += 32)
-                    qs[warp][x][d] = load_q(A.q, q_dtype, (u.row_start + tok) * A.q_stride + h * D + d);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) o[x][e] = 0.0f;
-            }
-            __syncwarp();
-            for (int t0 = u.k0; t0 < limit[3]; t0 += BT) {
-                const int slot = __ldg(A.page_table + (int64_t)u.seq * A.max_pages + (t0 >> 8));
-                if (slot < 0 || slot >= A.geo.n_pages) {
-                    if (lane == 0) status_or(A.status, KVQ_STATUS_BAD_SLOT);
-                    continue;
-                }
-                const uint8_t *page = A.pool + A.layer * A.geo.layer_stride + (int64_t)slot * A.geo.slot_stride + (int64_t)u.head * A.geo.page_bytes;
-                const uint8_t *tile = page + ((t0 >> 6) & 3) * BT_BYTES;
-                const float *sc = reinterpret_cast<const float *>(page + B_SCALES_OFF) + 2 * ((t0 >> 6) & 3);
-                float s[4][2] = {};
-                for (int c = 0; c < 16; ++c)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint4 w = *reinterpret_cast<const uint4 *>(tile + block_k_off(lane + 32 * j, 16 * c));
-                        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int b = 0; b < 8; ++b) {
-                            const float2 k = __half22float2(u32_as_h2(e4m3x2_to_h2((ww[b >> 1] >> (16 * (b & 1))) & 0xFFFFu)));
-#pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                s[x][j] = fmaf(qs[warp][x][16 * c + 2 * b + 1], k.y, fmaf(qs[warp][x][16 * c + 2 * b], k.x, s[x][j]));
-                        }
-                    }
-                const float f = sc[0] * (1.4426950408889634f / 16.0f), dv = sc[1];
-                __syncwarp();
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float a = t0 + lane < limit[x] ? s[x][0] * f : -INFINITY;
-                    const float b = t0 + lane + 32 < limit[x] ? s[x][1] * f : -INFINITY;
-                    float mx = fmaxf(a, b);
-#pragma unroll
-                    for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-                    const float mn = fmaxf(m[x], mx), ref = mn == -INFINITY ? 0.0f : mn;
-                    const float fac = exp2f(m[x] - ref), pa = exp2f(a - ref), pb = exp2f(b - ref);
-                    m[x] = mn;
-                    l[x] = l[x] * fac + pa + pb;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) o[x][e] *= fac;
-                    ps[warp][x][lane] = pa * dv;
-                    ps[warp][x][lane + 32] = pb * dv;
-                }
-                __syncwarp();
-                for (int k = 0; k < BT && t0 + k < limit[3]; ++k)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t code = tile[BT_K_BYTES + block_v_off(k, lane * 8 + e)];
-                        const float v = __low2float(u32_as_h2(e4m3x2_to_h2(code)));
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            if (t0 + k < limit[x]) o[x][e] = fmaf(ps[warp][x][k], v, o[x][e]);
-                    }
-                __syncwarp();
-            }
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                if (r + x >= n_rows) continue;
-#pragma unroll
-                for (int d = 16; d; d >>= 1) l[x] += __shfl_xor_sync(0xffffffffu, l[x], d);
-                if (u.slot >= 0) {
-                    float *w = A.ws + (int64_t)u.slot * PFB_SLOT;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) w[(rr + x) * D + lane * 8 + e] = o[x][e];
-                    if (lane == 0) w[PFB_ROWS * D + rr + x] = m[x], w[PFB_ROWS * (D + 1) + rr + x] = l[x];
-                } else {
-                    const float inv = l[x] > 0.0f ? 1.0f / l[x] : 0.0f;
-                    const int tok = (r + x) / A.G, h = u.head * A.G + (r + x) % A.G;
-                    const int64_t at = ((int64_t)(u.row_start + tok) * A.n_q_heads + h) * D + lane * 8;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        A.out_bf16[at + e] = __bfloat16_as_ushort(__float2bfloat16_rn(o[x][e] * inv));
-                        if (A.out_f32) A.out_f32[at + e] = o[x][e] * inv;
-                    }
-                }
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (std::is_same_v<T, __half>) {
+                const float2 f = __half22float2(u32_as_h2(w[i]));
+                x[2 * i] = f.x;
+                x[2 * i + 1] = f.y;
+            } else {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
             }
         }
     }
+}
+
+// Two pairs of weights (fp16) to three words of four E5M2 bytes.
+__device__ __forceinline__ void split_weights(uint32_t a, uint32_t b, uint32_t &t1, uint32_t &t2, uint32_t &t3) {
+    const uint32_t a1 = a + 0x00800080u, b1 = b + 0x00800080u;
+    t1 = __byte_perm(a1, b1, 0x7531);
+    const uint32_t ra = h2_as_u32(__hsub2(u32_as_h2(a), u32_as_h2(a1 & 0xFF00FF00u)));
+    const uint32_t rb = h2_as_u32(__hsub2(u32_as_h2(b), u32_as_h2(b1 & 0xFF00FF00u)));
+    const uint32_t a2 = ra + 0x00800080u, b2 = rb + 0x00800080u;
+    t2 = __byte_perm(a2, b2, 0x7531);
+    const uint32_t sa = h2_as_u32(__hsub2(u32_as_h2(ra), u32_as_h2(a2 & 0xFF00FF00u)));
+    const uint32_t sb = h2_as_u32(__hsub2(u32_as_h2(rb), u32_as_h2(b2 & 0xFF00FF00u)));
+    t3 = __byte_perm(sa + 0x00800080u, sb + 0x00800080u, 0x7531);
+}
+
+template <typename T, int TERMS>
+__global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A) {
+    using C = PfCfg<TERMS>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t *ring = sm + C::RING;
+    PfTail &X = *reinterpret_cast<PfTail *>(sm + C::TAIL);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < C::SLOTS; ++i) {
+            mbar_init(&X.full[i], 1);
+            mbar_init(&X.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&X.s_full[i], 1);
+            mbar_init(&X.p_full[i], PF_SOFT);
+        }
+        mbar_init(&X.o_done, 1);
+        mbar_init(&X.drained, 1);
+        mbar_init(&X.q_full, PF_SOFT);
+        X.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == PF_SOFT) tmem_alloc(&X.tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = X.tmem;
+    grid_dependency_wait();
+    const bool good = plan_ok(A);
+    const int32_t *start = A.plan + PLAN_HEADER + (int64_t)A.n_units * PFB_UNIT + (int64_t)A.n_merges * PFB_MERGE;
+    const int i0 = good ? max(0, start[blockIdx.x]) : 0, i1 = good ? min(A.n_units, start[blockIdx.x + 1]) : 0;
+    // A wait that gives up (2 s, or another role's did) raises the CTA's flag and the call's status.  From then on
+    // nothing is copied or multiplied and no wait waits, but every role walks its loop to the end: the warps' own
+    // barriers always find their partners.  Called by whole warps.
+    volatile int *abort_flag = &X.abort;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+        bool ok = mbar_try_wait(bar, parity);
+        if (!ok) {
+            const uint64_t t0 = globaltimer_ns();
+            while (!(ok = mbar_try_wait_sleep(bar, parity, 20000u))) {
+                if (*abort_flag) break;
+                if (globaltimer_ns() - t0 > PF_WAIT_NS) {
+                    *abort_flag = 1;
+                    status_or(A.status, KVQ_STATUS_TIMEOUT);
+                    break;
+                }
+            }
+        }
+        return __all_sync(0xffffffffu, ok) && !*abort_flag;
+    };
+
+    if (warp == PF_SOFT) {                       // ---- copies ----
+        const uint64_t base = reinterpret_cast<uint64_t>(A.pool) + A.layer * A.geo.layer_stride;
+        int op = 0;
+        bool ok = true;
+        for (int i = i0; i < i1 && ok; ++i) {
+            Unit u;
+            if (!load_unit(A, i, u)) continue;
+            const int nt = (u.k1 - u.k0 + PFB_KEYS - 1) / PFB_KEYS, kv_end = u.pos0 + u.n_tok;
+            const int32_t *row = A.page_table + (int64_t)u.seq * A.max_pages;
+            const int page0 = u.k0 >> 8, page_end = (u.k1 + PAGE - 1) >> 8;
+            // entries of 32 pages at a time, a window for K and, one step behind, V
+            int heldk = -1, heldv = -1, fromk = page0 - 32, fromv = page0 - 32;
+            auto slot_of = [&](int page, int &held, int &from) {
+                if (page >= from + 32) {
+                    from = page;
+                    held = page + lane < page_end ? __ldg(row + page + lane) : -1;
+                }
+                return __shfl_sync(0xffffffffu, held, page - from);
+            };
+            auto load = [&](int j, bool is_v) {
+                const int key = u.k0 + j * PFB_KEYS, s = op % C::SLOTS, use = op / C::SLOTS;
+                const int slot = is_v ? slot_of(key >> 8, heldv, fromv) : slot_of(key >> 8, heldk, fromk);
+                if (use > 0 && !wait(&X.empty[s], (use - 1) & 1)) return false;
+                if (lane == 0) {
+                    uint8_t *dst = ring + s * PF_SLOT_BYTES;
+                    if (slot >= 0 && slot < A.geo.n_pages) {
+                        const uint8_t *src = reinterpret_cast<const uint8_t *>(base) + (int64_t)slot * A.geo.slot_stride +
+                                             (int64_t)u.head * A.geo.page_bytes + ((key >> 6) & 3) * BT_BYTES;
+                        const int blocks = key + BT < kv_end ? 2 : 1;
+                        mbar_arrive_expect_tx(&X.full[s], blocks * BT_K_BYTES);
+                        for (int b = 0; b < blocks; ++b) {
+                            if (is_v) {
+                                bulk_g2s_plain(dst + b * BT_K_BYTES, src + b * BT_BYTES + BT_K_BYTES, BT_K_BYTES, &X.full[s]);
+                            } else {             // a dim half of both tiles lies together: 16 atoms, 1,024 bytes apart
+                                bulk_g2s_plain(dst + b * 8192, src + b * BT_BYTES, 8192, &X.full[s]);
+                                bulk_g2s_plain(dst + 16384 + b * 8192, src + b * BT_BYTES + 8192, 8192, &X.full[s]);
+                            }
+                        }
+                    } else {
+                        status_or(A.status, KVQ_STATUS_BAD_SLOT);
+                        mbar_arrive(&X.full[s]);
+                    }
+                }
+                __syncwarp();
+                ++op;
+                return true;
+            };
+            ok = load(0, false);
+            for (int j = 0; j < nt && ok; ++j) {
+                if (j + 1 < nt) ok = load(j + 1, false);
+                if (ok) ok = load(j, true);
+            }
+        }
+        // no copy is left in flight
+        for (int o = max(0, op - C::SLOTS); o < op; ++o)
+            mbar_wait_bounded(&X.full[o % C::SLOTS], (o / C::SLOTS) & 1, PF_WAIT_NS);
+    } else if (warp == PF_SOFT + 1) {            // ---- products ----
+        constexpr uint32_t ID_QK = umma_idesc_f8(128, 128, 0, 0), ID_PV = umma_idesc_f8(128, 256, 1, 0);
+        int op = 0, it = 0, un = 0;
+        bool ok = true;
+        const uint32_t q_at = smem_u32(sm), ring_at = smem_u32(ring);
+        for (int i = i0; i < i1 && ok; ++i) {
+            Unit u;
+            if (!load_unit(A, i, u)) continue;
+            const int nt = (u.k1 - u.k0 + PFB_KEYS - 1) / PFB_KEYS;
+            auto scores = [&](int step, int used) {        // used: the step whose weights these columns held, or a later one
+                const int s = op % C::SLOTS;
+                if (!wait(&X.full[s], (op / C::SLOTS) & 1)) return false;
+                if (used >= 0 && !wait(&X.o_done, used & 1)) return false;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t d = tmem + PF_S_COL + (step & 1) * 128, k = ring_at + s * PF_SLOT_BYTES;
+#pragma unroll
+                    for (int x = 0; x < TERMS * 8; ++x) {
+                        const uint32_t h = (x >> 2) & 1, off = (x & 3) * 32;
+                        umma_f8_ss(d, umma_desc(q_at + (x >> 3) * 32768 + h * 16384 + off, 1024, 2),
+                                   umma_desc(k + h * 16384 + off, 1024, 2), ID_QK, x > 0);
+                    }
+                    tc_commit(&X.s_full[step & 1]);
+                    tc_commit(&X.empty[s]);
+                }
+                __syncwarp();
+                ++op;
+                return true;
+            };
+            ok = wait(&X.q_full, un & 1);
+            ++un;
+            if (ok) ok = scores(it, it - 1);               // the last unit's products are all complete
+            for (int j = 0; j < nt && ok; ++j, ++it) {
+                if (j + 1 < nt) ok = scores(it + 1, it - 1);
+                const int s = op % C::SLOTS;
+                ok = ok && wait(&X.p_full[it & 1], (it >> 1) & 1) && wait(&X.full[s], (op / C::SLOTS) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint32_t p = tmem + PF_S_COL + (it & 1) * 128, v = ring_at + s * PF_SLOT_BYTES;
+#pragma unroll
+                    for (int x = 0; x < 12; ++x) {
+                        const int c = x / 3, term = x % 3;
+                        umma_f8_ts(tmem, p + 32 * c + 8 * term, umma_desc(v + (c >> 1) * BT_K_BYTES + (c & 1) * 32, 512, 4), ID_PV,
+                                   j > 0 || x > 0);
+                    }
+                    tc_commit(&X.empty[s]);
+                    tc_commit(&X.o_done);
+                }
+                __syncwarp();
+                ++op;
+            }
+        }
+        // every product is complete before TMEM goes back
+        if (lane == 0) tc_commit(&X.drained);
+        __syncwarp();
+        mbar_wait_bounded(&X.drained, 0, PF_WAIT_NS);
+    } else {                                     // ---- softmax ----
+        const int part = warp >> 2, row = 32 * (warp & 3) + lane, bar = 1 + (warp & 3);
+        const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const T *q = static_cast<const T *>(A.q);
+        int it = 0, op = 0;
+        for (int i = i0; i < i1; ++i) {
+            Unit u;
+            if (!load_unit(A, i, u)) continue;
+            const int n_rows = u.n_tok * A.G, nt = (u.k1 - u.k0 + PFB_KEYS - 1) / PFB_KEYS, kv_end = u.pos0 + u.n_tok;
+            // ---- query terms: rows 16 warp .. + 15, eight dims a lane ----
+#pragma unroll 1
+            for (int rr = 16 * warp; rr < 16 * warp + 16; rr += 4) {
+                float x[4][8];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    const int r = u.r0 + rr + y;
+                    if (r < n_rows) {
+                        load_q8(q + (int64_t)(u.row_start + r / A.G) * A.q_stride + (u.head * A.G + r % A.G) * D + lane * 8, x[y]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[y][e] = 0.0f;
+                    }
+                }
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    float mx = 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[y][e]));
+#pragma unroll
+                    for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                    const int kq = mx > 0.0f ? max(-114, min(114, 7 - ((int)(__float_as_uint(mx) >> 23) - 127))) : 0;
+                    const float up = pow2f(kq);
+                    if (lane == 0) X.qscale[rr + y] = pow2f(-kq) * (1.4426950408889634f / 16.0f);
+                    // dims 8 lane ..: half lane / 16, chunk (lane / 2) % 8, its low or high 8 bytes
+                    const int r = rr + y;
+                    uint8_t *dst = sm + (lane >> 4) * 16384 + (r >> 3) * 1024 + (r & 7) * 128 + ((((lane >> 1) & 7) ^ (r & 7)) << 4) + (lane & 1) * 8;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[y][e] *= up;
+#pragma unroll
+                    for (int t = 0; t < TERMS; ++t) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            w[e] = f32x2_to_e4m3x2(x[y][2 * e], x[y][2 * e + 1]);
+                            const float2 f = __half22float2(u32_as_h2(e4m3x2_to_h2(w[e])));
+                            x[y][2 * e] -= f.x;
+                            x[y][2 * e + 1] -= f.y;
+                        }
+                        *reinterpret_cast<uint2 *>(dst + t * 32768) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+                    }
+                }
+            }
+            fence_async_shared();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&X.q_full);
+            asm volatile("bar.sync 5, %0;" ::"n"(PF_SOFT * 32) : "memory");      // qscale of every row
+            const float qs = X.qscale[row];
+            const int r = u.r0 + row;
+            const int limit = r < n_rows ? min(u.k1, u.pos0 + r / A.G + 1) : u.k1;
+            const int low = min(u.k1, u.pos0 + u.r0 / A.G + 1);                  // keys below it are seen by every row
+            const int32_t *pt = A.page_table + (int64_t)u.seq * A.max_pages;
+            const uint8_t *kv = A.pool + A.layer * A.geo.layer_stride + (int64_t)u.head * A.geo.page_bytes + B_SCALES_OFF;
+            auto scales_at = [&](int slot, int key) {
+                if (slot < 0 || slot >= A.geo.n_pages) return make_float4(0.f, 0.f, 0.f, 0.f);
+                return __ldg(reinterpret_cast<const float4 *>(kv + (int64_t)slot * A.geo.slot_stride + ((key >> 7) & 1) * 16));
+            };
+            int slot = __ldg(pt + (u.k0 >> 8));
+            float4 sc = scales_at(slot, u.k0);
+            float m = -INFINITY, l = 0.0f;
+            int E = PF_NO_E;
+            for (int j = 0; j < nt; ++j, ++it) {
+                const int key0 = u.k0 + j * PFB_KEYS, mine = key0 + 64 * part;
+                const float4 now = sc;
+                const bool there = slot >= 0 && slot < A.geo.n_pages;
+                if (j + 1 < nt) {
+                    slot = __ldg(pt + ((key0 + PFB_KEYS) >> 8));
+                    sc = scales_at(slot, key0 + PFB_KEYS);
+                }
+                const bool two = key0 + BT < kv_end;
+                const float dk = part ? now.z : now.x;
+                const int ea = there && now.y > 0.0f ? (int)(__float_as_uint(now.y) >> 23) - 127 : PF_NO_E;
+                const int eb = there && two && now.w > 0.0f ? (int)(__float_as_uint(now.w) >> 23) - 127 : PF_NO_E;
+                const int ev = part ? eb : ea, En = max(E, max(ea, eb));
+                wait(&X.s_full[it & 1], (it >> 1) & 1);
+                tc_fence_after();
+                const uint32_t scol = tl + PF_S_COL + (it & 1) * 128 + 64 * part;
+                uint32_t s[64];
+                tmem_ld32<0>(scol, s);
+                tmem_ld32<32>(scol + 32, s);
+                tc_wait_ld();
+                // masked keys: past the row's limit, or in a page that is not there (their scores, and the scale of a
+                // tile that has no tokens, can be anything); a scale of 0 makes every score 0
+                const bool nonzero = dk > 0.0f;
+                if (!there || key0 + PFB_KEYS > low || !nonzero) {
+                    const int n = there ? limit - mine : 0;
+#pragma unroll
+                    for (int x = 0; x < 64; ++x) s[x] = x < n ? (nonzero ? s[x] : 0u) : 0xFF800000u;
+                }
+                const float f = nonzero ? fmaxf(qs * dk, FLT_MIN) : 1.0f;
+                float mx = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < 64; ++x) mx = fmaxf(mx, __uint_as_float(s[x]));
+                mx *= f;                                                         // f > 0
+                if (pair_any(mx > m + 3.0f || En > E, bar)) {
+                    X.red[part][row] = mx;
+                    asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
+                    const float mn = fmaxf(m, fmaxf(X.red[0][row], X.red[1][row]));
+                    const float fm = m == -INFINITY ? 0.0f : ex2(m - mn);
+                    if (j > 0) {
+                        wait(&X.o_done, (it - 1) & 1);
+                        tc_fence_after();
+                        const float fo = fm * (E == PF_NO_E ? 0.0f : pow2f(E - En));
+                        uint32_t o[32];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            tmem_ld32<0>(tl + 128 * part + 32 * c, o);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * fo);
+                            tmem_st32<0>(tl + 128 * part + 32 * c, o);
+                        }
+                    }
+                    l *= fm;
+                    m = mn;
+                    E = En;
+                }
+                // weights; a V scale far below the largest (or 0) would take the sum with it, so its factor comes after
+                const int c0 = ev - E >= -40 ? ev - E + 12 : 12;
+                const float late = ev - E >= -40 ? 1.0f : (ev == PF_NO_E ? 0.0f : pow2f(ev - E));
+                const float ref = (m == -INFINITY ? 0.0f : m) - (float)c0;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t t1[8], t2[8], t3[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        float w[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const float sv = __uint_as_float(s[32 * c + 4 * x + y]);
+                            w[y] = ex2(fmaf(sv, f, -ref));
+                            sum[y] += w[y];
+                        }
+                        if (late != 1.0f)
+#pragma unroll
+                            for (int y = 0; y < 4; ++y) w[y] *= late;
+                        split_weights(h2_as_u32(__floats2half2_rn(w[0], w[1])), h2_as_u32(__floats2half2_rn(w[2], w[3])), t1[x], t2[x], t3[x]);
+                    }
+                    tmem_st8(scol + 32 * c, t1);
+                    tmem_st8(scol + 32 * c + 8, t2);
+                    tmem_st8(scol + 32 * c + 16, t3);
+                }
+                l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) * pow2f(-c0);
+                // V codes that belong to no token (past the sequence's end, or of a page that is not there) may be
+                // NaN: they become zeros before the product
+                if (!there || key0 + PFB_KEYS > kv_end) {
+                    const int vop = op + (j < nt - 1 ? 2 * j + 2 : 2 * nt - 1);
+                    wait(&X.full[vop % C::SLOTS], (vop / C::SLOTS) & 1);
+                    uint8_t *v = ring + (vop % C::SLOTS) * PF_SLOT_BYTES + tid * 64;        // dim tid of the first tile
+                    const int n = there ? kv_end - key0 : 0;
+#pragma unroll 1
+                    for (int c = 0; c < 8; ++c) {
+                        const int have = n - 16 * c;
+                        if (have >= 16) continue;
+                        uint4 *p = reinterpret_cast<uint4 *>(v + (c >> 2) * BT_K_BYTES + (((c & 3) ^ ((tid >> 1) & 3)) << 4));
+                        uint4 w = *p;
+                        uint32_t b[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const int k = have - 4 * y;
+                            b[y] = k <= 0 ? 0u : (k >= 4 ? b[y] : b[y] & ((1u << (8 * k)) - 1u));
+                        }
+                        *p = make_uint4(b[0], b[1], b[2], b[3]);
+                    }
+                    fence_async_shared();
+                }
+                tc_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&X.p_full[it & 1]);
+            }
+            op += 2 * nt;
+            // ---- the unit's result ----
+            wait(&X.o_done, (it - 1) & 1);
+            tc_fence_after();
+            X.red[part][row] = l;
+            asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
+            l = X.red[0][row] + X.red[1][row];
+            const bool cut = u.slot >= 0;
+            const float unit_o = E == PF_NO_E ? 0.0f : exp2f((float)(E - 12));
+            const float fo = cut ? unit_o : (l > 0.0f ? unit_o / l : 0.0f);
+            const int tok = r / A.G;
+            const int64_t at = ((int64_t)(u.row_start + tok) * A.n_q_heads + u.head * A.G + (r - tok * A.G)) * D + 128 * part;
+            float *ws = A.ws + (int64_t)u.slot * PFB_SLOT;
+            if (cut && part == 0) {
+                ws[PFB_ROWS * D + row] = m;
+                ws[PFB_ROWS * (D + 1) + row] = l;
+            }
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                tmem_ld32<0>(tl + 128 * part + 32 * c, o);
+                tc_wait_ld();
+                if (r < n_rows && (cut || A.out_f32)) {
+                    float4 *dst = reinterpret_cast<float4 *>(cut ? ws + row * D + 128 * part + 32 * c : A.out_f32 + at + 32 * c);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        dst[x] = make_float4(__uint_as_float(o[4 * x]) * fo, __uint_as_float(o[4 * x + 1]) * fo,
+                                             __uint_as_float(o[4 * x + 2]) * fo, __uint_as_float(o[4 * x + 3]) * fo);
+                }
+                if (r < n_rows && !cut) {
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[2 * x]) * fo, __uint_as_float(o[2 * x + 1]) * fo);
+                        pk[x] = *reinterpret_cast<const uint32_t *>(&b);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        reinterpret_cast<uint4 *>(A.out_bf16 + at + 32 * c)[x] = make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == PF_SOFT) tmem_dealloc(tmem, 512);
 }
 
 // The parts of a cut row tile: M = max m, L = sum l 2^(m - M), o = sum o 2^(m - M) / L.
@@ -212,6 +596,22 @@ __global__ void __launch_bounds__(256) block_prefill_merge_kernel(PfbArgs A) {
     }
 }
 
+template <typename T, int TERMS> cudaError_t launch_prefill_typed(const PfbArgs &a, cudaStream_t s) {
+    static std::mutex mu;
+    static bool ready[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (!ready[dev]) {
+            const cudaError_t e = cudaFuncSetAttribute(block_prefill_kernel<T, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, PfCfg<TERMS>::SMEM);
+            if (e != cudaSuccess) return e;
+            ready[dev] = true;
+        }
+    }
+    return launch_ex(block_prefill_kernel<T, TERMS>, dim3((unsigned)a.n_ctas), dim3(PF_THREADS), PfCfg<TERMS>::SMEM, s, false, a);
+}
+
 }  // namespace
 
 cudaError_t launch_block_prefill(const uint8_t *pool, const PoolGeom &geo, int layer, const void *q, int q_dtype,
@@ -221,7 +621,9 @@ cudaError_t launch_block_prefill(const uint8_t *pool, const PoolGeom &geo, int l
     const PfbArgs a{pool, geo, layer, q, q_stride, page_table, max_pages, plan, info.n_units, info.n_seq, info.n_rows,
                     info.n_merges, info.n_slots, info.n_ctas, info.group, info.group * info.n_kv_heads, ws, status,
                     out_bf16, out_f32};
-    cudaError_t e = launch_ex(block_prefill_kernel, dim3((unsigned)info.n_ctas), dim3(PS_WARPS * 32), 0, s, false, a, q_dtype);
+    cudaError_t e = q_dtype == KVQ_BF16  ? launch_prefill_typed<__nv_bfloat16, 2>(a, s)
+                    : q_dtype == KVQ_F16 ? launch_prefill_typed<__half, 3>(a, s)
+                                         : launch_prefill_typed<float, 3>(a, s);
     if (e != cudaSuccess || info.n_merges == 0) return e;
     return launch_ex(block_prefill_merge_kernel, dim3((unsigned)info.n_merges * 16), dim3(256), 0, s, false, a);
 }

@@ -294,12 +294,15 @@ def decode(pool, q, table, lens, n_ctas=0, mode="combined", status=None, f32=Tru
     ws = torch.full((info.workspace_bytes // 4,), float("nan"), device="cuda")
     out = torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device="cuda")
     of = torch.full(q.shape, float("nan"), device="cuda") if f32 else None
+    own = status is None
+    status = i32([0]) if own else status
     if mode == "combined":
         kvq.paged_decode_attn_combined(pool, 0, q, table, dev(plan), info, ws, out, of, status)
     else:
         kvq.paged_decode_attn_fp8b(pool, 0, q, table, dev(plan), info, ws, status)
         kvq.attn_combine(ws, dev(plan), info, False, out, of)
     torch.cuda.synchronize()
+    assert not own or int(status.item()) == 0
     return out, of
 
 
@@ -406,8 +409,11 @@ def prefill(pool, q, table, pos0, toks, n_ctas=0, status=None):
     ws = torch.full((max(1, info.workspace_bytes // 4),), float("nan"), device="cuda")
     out = torch.full(q.shape, 7.0, dtype=torch.bfloat16, device="cuda")
     of = torch.full(q.shape, 7.0, device="cuda")
+    own = status is None
+    status = i32([0]) if own else status
     kvq.paged_prefill_attn_fp8b(pool, 0, q, table, dev(plan), info, ws, out, of, status)
     torch.cuda.synchronize()
+    assert not own or int(status.item()) == 0
     return out, of
 
 
