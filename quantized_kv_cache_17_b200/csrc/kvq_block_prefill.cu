@@ -139,6 +139,29 @@ template <typename T> __device__ __forceinline__ void load_q8(const T *p, float 
     }
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+// Two fp32 values in one 64-bit register: one instruction for both.
+__device__ __forceinline__ uint64_t pack_f2(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void unpack_f2(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma_f2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add_f2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 // Two pairs of weights (fp16) to three words of four E5M2 bytes.
 __device__ __forceinline__ void split_weights(uint32_t a, uint32_t b, uint32_t &t1, uint32_t &t2, uint32_t &t3) {
     const uint32_t a1 = a + 0x00800080u, b1 = b + 0x00800080u;
@@ -327,31 +350,35 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
             if (!load_unit(A, i, u)) continue;
             const int n_rows = u.n_tok * A.G, nt = (u.k1 - u.k0 + PFB_KEYS - 1) / PFB_KEYS, kv_end = u.pos0 + u.n_tok;
             // ---- query terms: rows 16 warp .. + 15, eight dims a lane ----
+            int64_t q_row = -1;                          // lane y < 16: where row 16 warp + y of the tile lies in q
+            if (lane < 16 && u.r0 + 16 * warp + lane < n_rows) {
+                const int r = u.r0 + 16 * warp + lane, tok = r / A.G;
+                q_row = (int64_t)(u.row_start + tok) * A.q_stride + (u.head * A.G + r - tok * A.G) * D;
+            }
 #pragma unroll 1
-            for (int rr = 16 * warp; rr < 16 * warp + 16; rr += 4) {
-                float x[4][8];
+            for (int yy = 0; yy < 16; yy += 8) {
+                float x[8][8];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int r = u.r0 + rr + y;
-                    if (r < n_rows) {
-                        load_q8(q + (int64_t)(u.row_start + r / A.G) * A.q_stride + (u.head * A.G + r % A.G) * D + lane * 8, x[y]);
+                for (int y = 0; y < 8; ++y) {
+                    const int64_t at = __shfl_sync(0xffffffffu, q_row, yy + y);
+                    if (at >= 0) {
+                        load_q8(q + at + lane * 8, x[y]);
                     } else {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) x[y][e] = 0.0f;
                     }
                 }
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
+                for (int y = 0; y < 8; ++y) {
+                    const int r = 16 * warp + yy + y;
                     float mx = 0.0f;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[y][e]));
-#pragma unroll
-                    for (int d = 16; d; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                    mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));   // not negative: the bits order as the values
                     const int kq = mx > 0.0f ? max(-114, min(114, 7 - ((int)(__float_as_uint(mx) >> 23) - 127))) : 0;
                     const float up = pow2f(kq);
-                    if (lane == 0) X.qscale[rr + y] = pow2f(-kq) * (1.4426950408889634f / 16.0f);
+                    if (lane == 0) X.qscale[r] = pow2f(-kq) * (1.4426950408889634f / 16.0f);
                     // dims 8 lane ..: half lane / 16, chunk (lane / 2) % 8, its low or high 8 bytes
-                    const int r = rr + y;
                     uint8_t *dst = sm + (lane >> 4) * 16384 + (r >> 3) * 1024 + (r & 7) * 128 + ((((lane >> 1) & 7) ^ (r & 7)) << 4) + (lane & 1) * 8;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[y][e] *= up;
@@ -383,7 +410,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
                 if (slot < 0 || slot >= A.geo.n_pages) return make_float4(0.f, 0.f, 0.f, 0.f);
                 return __ldg(reinterpret_cast<const float4 *>(kv + (int64_t)slot * A.geo.slot_stride + ((key >> 7) & 1) * 16));
             };
-            int slot = __ldg(pt + (u.k0 >> 8));
+            // a step's scales are loaded one step ahead, its page slot two
+            int slot = __ldg(pt + (u.k0 >> 8)), slot1 = nt > 1 ? __ldg(pt + ((u.k0 + PFB_KEYS) >> 8)) : -1;
             float4 sc = scales_at(slot, u.k0);
             float m = -INFINITY, l = 0.0f;
             int E = PF_NO_E;
@@ -391,10 +419,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
                 const int key0 = u.k0 + j * PFB_KEYS, mine = key0 + 64 * part;
                 const float4 now = sc;
                 const bool there = slot >= 0 && slot < A.geo.n_pages;
-                if (j + 1 < nt) {
-                    slot = __ldg(pt + ((key0 + PFB_KEYS) >> 8));
-                    sc = scales_at(slot, key0 + PFB_KEYS);
-                }
+                if (j + 1 < nt) sc = scales_at(slot1, key0 + PFB_KEYS);
+                slot = slot1;
+                if (j + 2 < nt) slot1 = __ldg(pt + ((key0 + 2 * PFB_KEYS) >> 8));
                 const bool two = key0 + BT < kv_end;
                 const float dk = part ? now.z : now.x;
                 const int ea = there && now.y > 0.0f ? (int)(__float_as_uint(now.y) >> 23) - 127 : PF_NO_E;
@@ -416,9 +443,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
                     for (int x = 0; x < 64; ++x) s[x] = x < n ? (nonzero ? s[x] : 0u) : 0xFF800000u;
                 }
                 const float f = nonzero ? fmaxf(qs * dk, FLT_MIN) : 1.0f;
-                float mx = -INFINITY;
+                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int x = 0; x < 64; ++x) mx = fmaxf(mx, __uint_as_float(s[x]));
+                for (int x = 0; x < 64; x += 2) mx4[(x >> 1) & 3] = max3(mx4[(x >> 1) & 3], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+                float mx = max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]);
                 mx *= f;                                                         // f > 0
                 if (pair_any(mx > m + 3.0f || En > E, bar)) {
                     X.red[part][row] = mx;
@@ -443,33 +471,43 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
                     m = mn;
                     E = En;
                 }
-                // weights; a V scale far below the largest (or 0) would take the sum with it, so its factor comes after
-                const int c0 = ev - E >= -40 ? ev - E + 12 : 12;
-                const float late = ev - E >= -40 ? 1.0f : (ev == PF_NO_E ? 0.0f : pow2f(ev - E));
-                const float ref = (m == -INFINITY ? 0.0f : m) - (float)c0;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                // The sum takes what the weights are made of.  A V scale so far below the largest (or 0) that the weights
+                // vanish would take the sum with it: it is made first then.
+                const int c0 = ev == PF_NO_E ? -200 : max(ev - E, -200) + 12;
+                const float ref = m == -INFINITY ? 0.0f : m;
+                if (c0 < -28) {
+#pragma unroll
+                    for (int x = 0; x < 64; ++x) l += ex2(fmaf(__uint_as_float(s[x]), f, -ref));
+                }
+                const uint64_t f2 = pack_f2(f, f), b2 = pack_f2((float)c0 - ref, (float)c0 - ref);
+                uint64_t sum[2] = {0, 0};
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     uint32_t t1[8], t2[8], t3[8];
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
-                        float w[4];
+                        uint32_t h[2];
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            const float sv = __uint_as_float(s[32 * c + 4 * x + y]);
-                            w[y] = ex2(fmaf(sv, f, -ref));
-                            sum[y] += w[y];
+                        for (int y = 0; y < 2; ++y) {
+                            const int at = 32 * c + 4 * x + 2 * y;
+                            float w0, w1;
+                            unpack_f2(fma_f2(pack_f2(__uint_as_float(s[at]), __uint_as_float(s[at + 1])), f2, b2), w0, w1);
+                            w0 = ex2(w0);
+                            w1 = ex2(w1);
+                            sum[y] = add_f2(sum[y], pack_f2(w0, w1));
+                            h[y] = h2_as_u32(__floats2half2_rn(w0, w1));
                         }
-                        if (late != 1.0f)
-#pragma unroll
-                            for (int y = 0; y < 4; ++y) w[y] *= late;
-                        split_weights(h2_as_u32(__floats2half2_rn(w[0], w[1])), h2_as_u32(__floats2half2_rn(w[2], w[3])), t1[x], t2[x], t3[x]);
+                        split_weights(h[0], h[1], t1[x], t2[x], t3[x]);
                     }
                     tmem_st8(scol + 32 * c, t1);
                     tmem_st8(scol + 32 * c + 8, t2);
                     tmem_st8(scol + 32 * c + 16, t3);
                 }
-                l += ((sum[0] + sum[1]) + (sum[2] + sum[3])) * pow2f(-c0);
+                if (c0 >= -28) {
+                    float a0, a1;
+                    unpack_f2(add_f2(sum[0], sum[1]), a0, a1);
+                    l += (a0 + a1) * pow2f(-c0);
+                }
                 // V codes that belong to no token (past the sequence's end, or of a page that is not there) may be
                 // NaN: they become zeros before the product
                 if (!there || key0 + PFB_KEYS > kv_end) {
@@ -509,25 +547,49 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
             const float unit_o = E == PF_NO_E ? 0.0f : exp2f((float)(E - 12));
             const float fo = cut ? unit_o : (l > 0.0f ? unit_o / l : 0.0f);
             const int tok = r / A.G;
-            const int64_t at = ((int64_t)(u.row_start + tok) * A.n_q_heads + u.head * A.G + (r - tok * A.G)) * D + 128 * part;
+            const int64_t at = r < n_rows ? ((int64_t)(u.row_start + tok) * A.n_q_heads + u.head * A.G + (r - tok * A.G)) * D : -1;
             float *ws = A.ws + (int64_t)u.slot * PFB_SLOT;
             if (cut && part == 0) {
                 ws[PFB_ROWS * D + row] = m;
                 ws[PFB_ROWS * (D + 1) + row] = l;
             }
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t o[32];
-                tmem_ld32<0>(tl + 128 * part + 32 * c, o);
-                tc_wait_ld();
-                if (r < n_rows && (cut || A.out_f32)) {
-                    float4 *dst = reinterpret_cast<float4 *>(cut ? ws + row * D + 128 * part + 32 * c : A.out_f32 + at + 32 * c);
-#pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        dst[x] = make_float4(__uint_as_float(o[4 * x]) * fo, __uint_as_float(o[4 * x + 1]) * fo,
-                                             __uint_as_float(o[4 * x + 2]) * fo, __uint_as_float(o[4 * x + 3]) * fo);
+            // Through the query's shared memory (its products are complete), so that a warp stores 512 bytes of one row at
+            // a time: a row's 16-byte chunks are XORed with the row, which keeps both sides free of bank conflicts.
+            auto put = [&](int chunk, const uint4 &v) { *reinterpret_cast<uint4 *>(sm + row * 512 + ((chunk ^ (row & 7)) << 4)) = v; };
+            auto rows_out = [&](auto store) {            // the pair's 32 rows, 16 a warp; lane = chunk
+                asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
+#pragma unroll 4
+                for (int y = 16 * part; y < 16 * part + 16; ++y) {
+                    const int rr = 32 * (warp & 3) + y;
+                    const int64_t to = __shfl_sync(0xffffffffu, at, y);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(sm + rr * 512 + ((lane ^ (rr & 7)) << 4));
+                    if (to >= 0) store(rr, to, v);
                 }
-                if (r < n_rows && !cut) {
+                asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
+            };
+            if (cut || A.out_f32) {
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {            // 64 columns of each half a round
+                    uint32_t o[64];
+                    tmem_ld32<0>(tl + 128 * part + 64 * h, o);
+                    tmem_ld32<32>(tl + 128 * part + 64 * h + 32, o);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int x = 0; x < 64; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * fo);
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) put(16 * part + x, make_uint4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]));
+                    rows_out([&](int rr, int64_t to, const uint4 &v) {
+                        float *dst = (cut ? ws + rr * D : A.out_f32 + to) + 128 * (lane >> 4) + 64 * h + 4 * (lane & 15);
+                        *reinterpret_cast<uint4 *>(dst) = v;
+                    });
+                }
+            }
+            if (!cut) {
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32<0>(tl + 128 * part + 32 * c, o);
+                    tc_wait_ld();
                     uint32_t pk[16];
 #pragma unroll
                     for (int x = 0; x < 16; ++x) {
@@ -535,11 +597,11 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
                         pk[x] = *reinterpret_cast<const uint32_t *>(&b);
                     }
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        reinterpret_cast<uint4 *>(A.out_bf16 + at + 32 * c)[x] = make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
+                    for (int x = 0; x < 4; ++x) put(16 * part + 4 * c + x, make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]));
                 }
-                __syncwarp();
+                rows_out([&](int, int64_t to, const uint4 &v) { *reinterpret_cast<uint4 *>(A.out_bf16 + to + 8 * lane) = v; });
             }
+            asm volatile("bar.sync 5, %0;" ::"n"(PF_SOFT * 32) : "memory");      // the next query goes where the rows were
             tc_fence_before();
         }
     }
