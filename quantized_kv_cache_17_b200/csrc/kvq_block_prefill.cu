@@ -52,13 +52,15 @@ __device__ __forceinline__ bool plan_ok(const PfbArgs &A) {
 }
 
 // ---------------------------------------------------------------------------
-// The kernel: one CTA per SM, 320 threads, walking its units.
+// The kernel: one CTA per SM, 384 threads, walking its units.
 //   warps 0-7  softmax.  Warp w and warp w + 4 share the 32 rows 32 (w % 4) ..; a
 //              thread has one row and 64 of a step's 128 keys, one 64-token tile
 //              and so one K and one V scale.
-//   warp 8     bulk copies of K and V codes into a ring of 32 KB slots, in the
-//              order the tensor core uses them: K0 K1 V0 K2 V1 ...
-//   warp 9     one lane issues every tcgen05.mma.
+//   warps 8, 9    bulk copies of K and of V codes, each into a ring of 32 KB slots
+//   warps 10, 11  one lane issues the scores' products, one the values': each waits
+//                 for its own operands while the other's are in the tensor cores
+// The copy and product warps' warpgroup gives registers to the softmax's two
+// (setmaxnreg): at the 168 that 384 threads get, the softmax loop spilled.
 // Both products take the codes as they lie in the pool (kind::f8f6f4, B operand):
 //   S[128 rows][128 keys] = sum over terms of Q_i K^T: a row of Q, scaled so that
 //     its largest value lies in [2^7, 2^8), is a sum of E4M3 terms, each the
@@ -75,27 +77,32 @@ __device__ __forceinline__ bool plan_ok(const PfbArgs &A) {
 // reference, e_v the exponent of the tile's V scale and E the largest e_v of the
 // unit so far, so V scales cost nothing.  m moves only when a score passes it by
 // 2^3: then, or when E moves, the row's O is multiplied in TMEM.
-// TMEM, all 512 columns: O 0-255; S of even steps 256-383, of odd ones 384-511.
-// The weights of the 32 keys c overwrite their scores: term i at 32 c + 8 i.
-// Two products that touch the same S / P columns (the values of step j, the scores
-// of step j + 2) are ordered by a wait on the former's commit.
+// TMEM: O 0-255, S 256-383, weights 384-479 (term i of the 32 keys c at
+// 384 + 24 c + 8 i); all 512 columns are allocated.  The scores of step j + 1 are
+// made as soon as the softmax has step j's in registers, behind the values of step
+// j - 1 in the tensor cores' queue, so the softmax runs from step to step.  (Two
+// score buffers with the weights over the scores need as many columns and make
+// the scores of step j + 2 wait for the values of step j: 3,610 cycles a step.)
 // ---------------------------------------------------------------------------
 constexpr int PF_SOFT = 8;                       // softmax warps
-constexpr int PF_THREADS = (PF_SOFT + 2) * 32;
+constexpr int PF_THREADS = (PF_SOFT + 4) * 32;     // three warpgroups
+constexpr int PF_REGS = 168;                     // a thread's registers at launch: what 384 threads can have
+constexpr int PF_REGS_SOFT = 208, PF_REGS_REST = 88;
+static_assert(2 * PF_REGS_SOFT + PF_REGS_REST <= 3 * PF_REGS, "the softmax warps take what the others give back");
 constexpr int PF_SLOT_BYTES = 32768;
 constexpr uint64_t PF_WAIT_NS = 2000000000ull;
-constexpr int PF_S_COL = 256;
+constexpr int PF_S_COL = 256, PF_P_COL = 384;
 constexpr int PF_NO_E = -10000;
 
 template <int TERMS> struct PfCfg {
-    static constexpr int SLOTS = TERMS == 2 ? 5 : 4;
+    static constexpr int K_SLOTS = 2, V_SLOTS = TERMS == 2 ? 3 : 2;
     static constexpr int Q_BYTES = TERMS * 32768;
     static constexpr int RING = Q_BYTES;
-    static constexpr int TAIL = RING + SLOTS * PF_SLOT_BYTES;
+    static constexpr int TAIL = RING + (K_SLOTS + V_SLOTS) * PF_SLOT_BYTES;
     static constexpr int SMEM = TAIL + 2048 + 1024;         // the tail; the ring starts on an atom's boundary
 };
 struct PfTail {
-    uint64_t full[5], empty[5], s_full[2], p_full[2], o_done, q_full, drained;
+    uint64_t k_full[2], k_empty[2], v_full[3], v_empty[3], s_full, s_free, p_full, o_done, q_full, drained;
     uint32_t tmem;
     int abort;
     float qscale[PFB_ROWS];
@@ -144,6 +151,18 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
+// Loads that stay where they are written: a plain load was moved to its use, a
+// step later, and cost every step its latency (1,200 cycles).
+__device__ __forceinline__ float4 ld_now(const float4 *p) {
+    float4 v;
+    asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ int ld_now(const int32_t *p) {
+    int v;
+    asm volatile("ld.global.nc.s32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
 // Two fp32 values in one 64-bit register: one instruction for both.
 __device__ __forceinline__ uint64_t pack_f2(float a, float b) {
     uint64_t d;
@@ -180,20 +199,22 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
     using C = PfCfg<TERMS>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-    uint8_t *ring = sm + C::RING;
     PfTail &X = *reinterpret_cast<PfTail *>(sm + C::TAIL);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
-        for (int i = 0; i < C::SLOTS; ++i) {
-            mbar_init(&X.full[i], 1);
-            mbar_init(&X.empty[i], 1);
+        for (int i = 0; i < C::K_SLOTS; ++i) {
+            mbar_init(&X.k_full[i], 1);
+            mbar_init(&X.k_empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&X.s_full[i], 1);
-            mbar_init(&X.p_full[i], PF_SOFT);
+        for (int i = 0; i < C::V_SLOTS; ++i) {
+            mbar_init(&X.v_full[i], 1);
+            mbar_init(&X.v_empty[i], 1);
         }
+        mbar_init(&X.s_full, 1);
+        mbar_init(&X.s_free, PF_SOFT);
+        mbar_init(&X.p_full, PF_SOFT);
         mbar_init(&X.o_done, 1);
-        mbar_init(&X.drained, 1);
+        mbar_init(&X.drained, 2);
         mbar_init(&X.q_full, PF_SOFT);
         X.abort = 0;
         fence_mbar_init();
@@ -227,124 +248,143 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
         return __all_sync(0xffffffffu, ok) && !*abort_flag;
     };
 
-    if (warp == PF_SOFT) {                       // ---- copies ----
-        const uint64_t base = reinterpret_cast<uint64_t>(A.pool) + A.layer * A.geo.layer_stride;
-        int op = 0;
+    if (warp >= PF_SOFT) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(PF_REGS_REST));
+        const bool is_v = warp & 1;                          // warps 8 and 10: K; 9 and 11: V
+        const int slots = is_v ? C::V_SLOTS : C::K_SLOTS;
+        uint64_t *full = is_v ? X.v_full : X.k_full, *empty = is_v ? X.v_empty : X.k_empty;
+        uint8_t *ring = sm + C::RING + (is_v ? C::K_SLOTS * PF_SLOT_BYTES : 0);
+        int slot = 0, it = 0, un = 0;
+        uint32_t phase = 0;                                  // of the ring
         bool ok = true;
-        for (int i = i0; i < i1 && ok; ++i) {
-            Unit u;
-            if (!load_unit(A, i, u)) continue;
-            const int nt = (u.k1 - u.k0 + PFB_KEYS - 1) / PFB_KEYS, kv_end = u.pos0 + u.n_tok;
-            const int32_t *row = A.page_table + (int64_t)u.seq * A.max_pages;
-            const int page0 = u.k0 >> 8, page_end = (u.k1 + PAGE - 1) >> 8;
-            // entries of 32 pages at a time, a window for K and, one step behind, V
-            int heldk = -1, heldv = -1, fromk = page0 - 32, fromv = page0 - 32;
-            auto slot_of = [&](int page, int &held, int &from) {
-                if (page >= from + 32) {
-                    from = page;
-                    held = page + lane < page_end ? __ldg(row + page + lane) : -1;
-                }
-                return __shfl_sync(0xffffffffu, held, page - from);
-            };
-            auto load = [&](int j, bool is_v) {
-                const int key = u.k0 + j * PFB_KEYS, s = op % C::SLOTS, use = op / C::SLOTS;
-                const int slot = is_v ? slot_of(key >> 8, heldv, fromv) : slot_of(key >> 8, heldk, fromk);
-                if (use > 0 && !wait(&X.empty[s], (use - 1) & 1)) return false;
-                if (lane == 0) {
-                    uint8_t *dst = ring + s * PF_SLOT_BYTES;
-                    if (slot >= 0 && slot < A.geo.n_pages) {
-                        const uint8_t *src = reinterpret_cast<const uint8_t *>(base) + (int64_t)slot * A.geo.slot_stride +
-                                             (int64_t)u.head * A.geo.page_bytes + ((key >> 6) & 3) * BT_BYTES;
-                        const int blocks = key + BT < kv_end ? 2 : 1;
-                        mbar_arrive_expect_tx(&X.full[s], blocks * BT_K_BYTES);
-                        for (int b = 0; b < blocks; ++b) {
-                            if (is_v) {
-                                bulk_g2s_plain(dst + b * BT_K_BYTES, src + b * BT_BYTES + BT_K_BYTES, BT_K_BYTES, &X.full[s]);
-                            } else {             // a dim half of both tiles lies together: 16 atoms, 1,024 bytes apart
-                                bulk_g2s_plain(dst + b * 8192, src + b * BT_BYTES, 8192, &X.full[s]);
-                                bulk_g2s_plain(dst + 16384 + b * 8192, src + b * BT_BYTES + 8192, 8192, &X.full[s]);
+        auto next_slot = [&]() {
+            if (++slot == slots) slot = 0, phase ^= 1;
+        };
+        if (warp < PF_SOFT + 2) {                            // ---- copies ----
+            const uint8_t *base = A.pool + A.layer * A.geo.layer_stride;
+            for (int i = i0; i < i1 && ok; ++i) {
+                Unit u;
+                if (!load_unit(A, i, u)) continue;
+                const int nt = (u.k1 - u.k0 + PFB_KEYS - 1) / PFB_KEYS, kv_end = u.pos0 + u.n_tok;
+                const int32_t *row = A.page_table + (int64_t)u.seq * A.max_pages;
+                const int page_end = (u.k1 + PAGE - 1) >> 8;
+                int held = -1, from = (u.k0 >> 8) - 32;      // entries of 32 pages at a time
+                for (int j = 0; j < nt; ++j, ++it) {
+                    const int key = u.k0 + j * PFB_KEYS, page = key >> 8;
+                    if (page >= from + 32) {
+                        from = page;
+                        held = page + lane < page_end ? __ldg(row + page + lane) : -1;
+                    }
+                    const int at = __shfl_sync(0xffffffffu, held, page - from);
+                    if (it >= slots && !wait(&empty[slot], phase ^ 1)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lane == 0) {
+                        uint8_t *dst = ring + slot * PF_SLOT_BYTES;
+                        if (at >= 0 && at < A.geo.n_pages) {
+                            const uint8_t *src = base + (int64_t)at * A.geo.slot_stride + (int64_t)u.head * A.geo.page_bytes +
+                                                 ((key >> 6) & 3) * BT_BYTES;
+                            const int blocks = key + BT < kv_end ? 2 : 1;
+                            mbar_arrive_expect_tx(&full[slot], blocks * BT_K_BYTES);
+                            for (int b = 0; b < blocks; ++b) {
+                                if (is_v) {
+                                    bulk_g2s_plain(dst + b * BT_K_BYTES, src + b * BT_BYTES + BT_K_BYTES, BT_K_BYTES, &full[slot]);
+                                } else {         // a dim half of both tiles lies together: 16 atoms, 1,024 bytes apart
+                                    bulk_g2s_plain(dst + b * 8192, src + b * BT_BYTES, 8192, &full[slot]);
+                                    bulk_g2s_plain(dst + 16384 + b * 8192, src + b * BT_BYTES + 8192, 8192, &full[slot]);
+                                }
                             }
+                        } else {
+                            status_or(A.status, KVQ_STATUS_BAD_SLOT);
+                            mbar_arrive(&full[slot]);
                         }
-                    } else {
-                        status_or(A.status, KVQ_STATUS_BAD_SLOT);
-                        mbar_arrive(&X.full[s]);
+                    }
+                    __syncwarp();
+                    next_slot();
+                }
+            }
+            for (int o = max(0, it - slots); o < it; ++o)    // no copy is left in flight
+                mbar_wait_bounded(&full[o % slots], (o / slots) & 1, PF_WAIT_NS);
+        } else if (lane == 0) {                              // ---- products: one lane, a warp for each of the two ----
+            constexpr uint32_t ID_QK = umma_idesc_f8(128, 128, 0, 0), ID_PV = umma_idesc_f8(128, 256, 1, 0);
+            const uint64_t q_desc = umma_desc(smem_u32(sm), 1024, 2), k_desc = umma_desc(smem_u32(ring), 1024, 2),
+                           v_desc = umma_desc(smem_u32(ring), 512, 4);
+            auto wait1 = [&](uint64_t *bar, uint32_t parity) {
+                if (mbar_try_wait(bar, parity)) return true;
+                const uint64_t t0 = globaltimer_ns();
+                while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
+                    if (*abort_flag) return false;
+                    if (globaltimer_ns() - t0 > PF_WAIT_NS) {
+                        *abort_flag = 1;
+                        status_or(A.status, KVQ_STATUS_TIMEOUT);
+                        return false;
                     }
                 }
-                __syncwarp();
-                ++op;
                 return true;
             };
-            ok = load(0, false);
-            for (int j = 0; j < nt && ok; ++j) {
-                if (j + 1 < nt) ok = load(j + 1, false);
-                if (ok) ok = load(j, true);
-            }
-        }
-        // no copy is left in flight
-        for (int o = max(0, op - C::SLOTS); o < op; ++o)
-            mbar_wait_bounded(&X.full[o % C::SLOTS], (o / C::SLOTS) & 1, PF_WAIT_NS);
-    } else if (warp == PF_SOFT + 1) {            // ---- products ----
-        constexpr uint32_t ID_QK = umma_idesc_f8(128, 128, 0, 0), ID_PV = umma_idesc_f8(128, 256, 1, 0);
-        int op = 0, it = 0, un = 0;
-        bool ok = true;
-        const uint32_t q_at = smem_u32(sm), ring_at = smem_u32(ring);
-        for (int i = i0; i < i1 && ok; ++i) {
-            Unit u;
-            if (!load_unit(A, i, u)) continue;
-            const int nt = (u.k1 - u.k0 + PFB_KEYS - 1) / PFB_KEYS;
-            auto scores = [&](int step, int used) {        // used: the step whose weights these columns held, or a later one
-                const int s = op % C::SLOTS;
-                if (!wait(&X.full[s], (op / C::SLOTS) & 1)) return false;
-                if (used >= 0 && !wait(&X.o_done, used & 1)) return false;
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t d = tmem + PF_S_COL + (step & 1) * 128, k = ring_at + s * PF_SLOT_BYTES;
+            for (int i = i0; i < i1 && ok; ++i) {
+                Unit u;
+                if (!load_unit(A, i, u)) continue;
+                const int nt = (u.k1 - u.k0 + PFB_KEYS - 1) / PFB_KEYS;
+                if (!is_v) ok = wait1(&X.q_full, un & 1);
+                ++un;
+                for (int j = 0; j < nt && ok; ++j, ++it) {
+                    ok = wait1(&full[slot], phase);
+                    if (is_v) {                              // values: the weights are written
+                        if (!ok || !wait1(&X.p_full, it & 1)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t v = v_desc + slot * (PF_SLOT_BYTES >> 4);
 #pragma unroll
-                    for (int x = 0; x < TERMS * 8; ++x) {
-                        const uint32_t h = (x >> 2) & 1, off = (x & 3) * 32;
-                        umma_f8_ss(d, umma_desc(q_at + (x >> 3) * 32768 + h * 16384 + off, 1024, 2),
-                                   umma_desc(k + h * 16384 + off, 1024, 2), ID_QK, x > 0);
-                    }
-                    tc_commit(&X.s_full[step & 1]);
-                    tc_commit(&X.empty[s]);
-                }
-                __syncwarp();
-                ++op;
-                return true;
-            };
-            ok = wait(&X.q_full, un & 1);
-            ++un;
-            if (ok) ok = scores(it, it - 1);               // the last unit's products are all complete
-            for (int j = 0; j < nt && ok; ++j, ++it) {
-                if (j + 1 < nt) ok = scores(it + 1, it - 1);
-                const int s = op % C::SLOTS;
-                ok = ok && wait(&X.p_full[it & 1], (it >> 1) & 1) && wait(&X.full[s], (op / C::SLOTS) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint32_t p = tmem + PF_S_COL + (it & 1) * 128, v = ring_at + s * PF_SLOT_BYTES;
+                        for (int x = 0; x < 12; ++x) {
+                            const int c = x / 3, term = x % 3;
+                            umma_f8_ts(tmem, tmem + PF_P_COL + 24 * c + 8 * term, v + (((c >> 1) * BT_K_BYTES + (c & 1) * 32) >> 4), ID_PV,
+                                       j > 0 || x > 0);
+                        }
+                        tc_commit(&X.o_done);
+                    } else {                                 // scores: the ones before have been read
+                        if (!ok || (it > 0 && !wait1(&X.s_free, (it - 1) & 1))) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t k = k_desc + slot * (PF_SLOT_BYTES >> 4);
 #pragma unroll
-                    for (int x = 0; x < 12; ++x) {
-                        const int c = x / 3, term = x % 3;
-                        umma_f8_ts(tmem, p + 32 * c + 8 * term, umma_desc(v + (c >> 1) * BT_K_BYTES + (c & 1) * 32, 512, 4), ID_PV,
-                                   j > 0 || x > 0);
+                        for (int x = 0; x < TERMS * 8; ++x) {
+                            const uint64_t off = (((x >> 2) & 1) * 16384 + (x & 3) * 32) >> 4;
+                            umma_f8_ss(tmem + PF_S_COL, q_desc + ((x >> 3) * 32768 >> 4) + off, k + off, ID_QK, x > 0);
+                        }
+                        tc_commit(&X.s_full);
                     }
-                    tc_commit(&X.empty[s]);
-                    tc_commit(&X.o_done);
+                    tc_commit(&empty[slot]);
+                    next_slot();
                 }
-                __syncwarp();
-                ++op;
             }
+            tc_commit(&X.drained);                           // every product is complete before TMEM goes back
+            mbar_wait_bounded(&X.drained, 0, PF_WAIT_NS);
         }
-        // every product is complete before TMEM goes back
-        if (lane == 0) tc_commit(&X.drained);
         __syncwarp();
-        mbar_wait_bounded(&X.drained, 0, PF_WAIT_NS);
     } else {                                     // ---- softmax ----
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PF_REGS_SOFT));
         const int part = warp >> 2, row = 32 * (warp & 3) + lane, bar = 1 + (warp & 3);
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         const T *q = static_cast<const T *>(A.q);
-        int it = 0, op = 0;
+        int it = 0;
+        auto wait_s = [&](uint64_t *bar, uint32_t parity) {     // as wait, without its answer
+            if (!mbar_try_wait(bar, parity)) {
+                const uint64_t t0 = globaltimer_ns();
+                while (!mbar_try_wait_sleep(bar, parity, 20000u) && !*abort_flag) {
+                    if (globaltimer_ns() - t0 > PF_WAIT_NS) {
+                        *abort_flag = 1;
+                        status_or(A.status, KVQ_STATUS_TIMEOUT);
+                    }
+                }
+            }
+            __syncwarp();
+        };
         for (int i = i0; i < i1; ++i) {
             Unit u;
             if (!load_unit(A, i, u)) continue;
@@ -406,34 +446,53 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
             const int low = min(u.k1, u.pos0 + u.r0 / A.G + 1);                  // keys below it are seen by every row
             const int32_t *pt = A.page_table + (int64_t)u.seq * A.max_pages;
             const uint8_t *kv = A.pool + A.layer * A.geo.layer_stride + (int64_t)u.head * A.geo.page_bytes + B_SCALES_OFF;
-            auto scales_at = [&](int slot, int key) {
-                if (slot < 0 || slot >= A.geo.n_pages) return make_float4(0.f, 0.f, 0.f, 0.f);
-                return __ldg(reinterpret_cast<const float4 *>(kv + (int64_t)slot * A.geo.slot_stride + ((key >> 7) & 1) * 16));
+            // What a step needs of its tiles' scales is the same for every row: lane i works it out for step i of 32, and a
+            // step takes it from there.  rec_k: this half's K scale, negative where the page is not there.  rec_v: E of the
+            // step (its largest V exponent so far) in the high half, the exponent of this half's weights, V scale included,
+            // in the low one.  The next 32 steps' page slots and scales are loaded while these are used.
+            auto load_slot = [&](int j) { return j < nt ? ld_now(pt + ((u.k0 + j * PFB_KEYS) >> 8)) : -1; };
+            auto load_scales = [&](int slot, int j) {
+                if (slot < 0 || slot >= A.geo.n_pages) return make_float4(-1.0f, 0.f, -1.0f, 0.f);
+                return ld_now(reinterpret_cast<const float4 *>(kv + (int64_t)slot * A.geo.slot_stride + (((u.k0 >> 7) + j) & 1) * 16));
             };
-            // a step's scales are loaded one step ahead, its page slot two
-            int slot = __ldg(pt + (u.k0 >> 8)), slot1 = nt > 1 ? __ldg(pt + ((u.k0 + PFB_KEYS) >> 8)) : -1;
-            float4 sc = scales_at(slot, u.k0);
+            int slot = load_slot(lane);
+            float4 sc = load_scales(slot, lane);
+            float rec_k = 0.0f;
+            int rec_v = 0;
             float m = -INFINITY, l = 0.0f;
             int E = PF_NO_E;
             for (int j = 0; j < nt; ++j, ++it) {
                 const int key0 = u.k0 + j * PFB_KEYS, mine = key0 + 64 * part;
-                const float4 now = sc;
-                const bool there = slot >= 0 && slot < A.geo.n_pages;
-                if (j + 1 < nt) sc = scales_at(slot1, key0 + PFB_KEYS);
-                slot = slot1;
-                if (j + 2 < nt) slot1 = __ldg(pt + ((key0 + 2 * PFB_KEYS) >> 8));
-                const bool two = key0 + BT < kv_end;
-                const float dk = part ? now.z : now.x;
-                const int ea = there && now.y > 0.0f ? (int)(__float_as_uint(now.y) >> 23) - 127 : PF_NO_E;
-                const int eb = there && two && now.w > 0.0f ? (int)(__float_as_uint(now.w) >> 23) - 127 : PF_NO_E;
-                const int ev = part ? eb : ea, En = max(E, max(ea, eb));
-                wait(&X.s_full[it & 1], (it >> 1) & 1);
+                if ((j & 31) == 0) {
+                    const int step = j + lane;
+                    auto exponent = [](float x) { return x > 0.0f ? (int)(__float_as_uint(x) >> 23) - 127 : PF_NO_E; };
+                    const int ea = exponent(sc.y), eb = u.k0 + step * PFB_KEYS + BT < kv_end ? exponent(sc.w) : PF_NO_E;
+                    int top = step < nt ? max(ea, eb) : PF_NO_E;
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const int o = __shfl_up_sync(0xffffffffu, top, d);
+                        if (lane >= d) top = max(top, o);
+                    }
+                    top = max(top, E);
+                    const int ev = part ? eb : ea;
+                    rec_k = part ? sc.z : sc.x;
+                    rec_v = (top << 16) | ((ev == PF_NO_E ? -188 : max(ev - top, -200) + 12) & 0xFFFF);
+                    slot = load_slot(step + 32);
+                }
+                if ((j & 31) == 16) sc = load_scales(slot, (j & ~31) + 32 + lane);
+                const float dk = __shfl_sync(0xffffffffu, rec_k, j & 31);
+                const int rv = __shfl_sync(0xffffffffu, rec_v, j & 31), En = rv >> 16, c0 = (int)(short)(rv & 0xFFFF);
+                const bool there = !(dk < 0.0f);
+                wait_s(&X.s_full, it & 1);
                 tc_fence_after();
-                const uint32_t scol = tl + PF_S_COL + (it & 1) * 128 + 64 * part;
+                const uint32_t scol = tl + PF_S_COL + 64 * part, pcol = tl + PF_P_COL + 48 * part;
                 uint32_t s[64];
                 tmem_ld32<0>(scol, s);
                 tmem_ld32<32>(scol + 32, s);
                 tc_wait_ld();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&X.s_free);
                 // masked keys: past the row's limit, or in a page that is not there (their scores, and the scale of a
                 // tile that has no tokens, can be anything); a scale of 0 makes every score 0
                 const bool nonzero = dk > 0.0f;
@@ -454,7 +513,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
                     const float mn = fmaxf(m, fmaxf(X.red[0][row], X.red[1][row]));
                     const float fm = m == -INFINITY ? 0.0f : ex2(m - mn);
                     if (j > 0) {
-                        wait(&X.o_done, (it - 1) & 1);
+                        wait_s(&X.o_done, (it - 1) & 1);
                         tc_fence_after();
                         const float fo = fm * (E == PF_NO_E ? 0.0f : pow2f(E - En));
                         uint32_t o[32];
@@ -473,7 +532,6 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
                 }
                 // The sum takes what the weights are made of.  A V scale so far below the largest (or 0) that the weights
                 // vanish would take the sum with it: it is made first then.
-                const int c0 = ev == PF_NO_E ? -200 : max(ev - E, -200) + 12;
                 const float ref = m == -INFINITY ? 0.0f : m;
                 if (c0 < -28) {
 #pragma unroll
@@ -481,9 +539,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
                 }
                 const uint64_t f2 = pack_f2(f, f), b2 = pack_f2((float)c0 - ref, (float)c0 - ref);
                 uint64_t sum[2] = {0, 0};
+                uint32_t t[48];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    uint32_t t1[8], t2[8], t3[8];
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
                         uint32_t h[2];
@@ -497,23 +555,26 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
                             sum[y] = add_f2(sum[y], pack_f2(w0, w1));
                             h[y] = h2_as_u32(__floats2half2_rn(w0, w1));
                         }
-                        split_weights(h[0], h[1], t1[x], t2[x], t3[x]);
+                        split_weights(h[0], h[1], t[24 * c + x], t[24 * c + 8 + x], t[24 * c + 16 + x]);
                     }
-                    tmem_st8(scol + 32 * c, t1);
-                    tmem_st8(scol + 32 * c + 8, t2);
-                    tmem_st8(scol + 32 * c + 16, t3);
                 }
                 if (c0 >= -28) {
                     float a0, a1;
                     unpack_f2(add_f2(sum[0], sum[1]), a0, a1);
                     l += (a0 + a1) * pow2f(-c0);
                 }
+                if (j > 0) {                             // the weights before have been used
+                    wait_s(&X.o_done, (it - 1) & 1);
+                    tc_fence_after();
+                }
+                tmem_st32<0>(pcol, t);
+                tmem_st16<32>(pcol + 32, t);
                 // V codes that belong to no token (past the sequence's end, or of a page that is not there) may be
                 // NaN: they become zeros before the product
                 if (!there || key0 + PFB_KEYS > kv_end) {
-                    const int vop = op + (j < nt - 1 ? 2 * j + 2 : 2 * nt - 1);
-                    wait(&X.full[vop % C::SLOTS], (vop / C::SLOTS) & 1);
-                    uint8_t *v = ring + (vop % C::SLOTS) * PF_SLOT_BYTES + tid * 64;        // dim tid of the first tile
+                    const int vs = it % C::V_SLOTS;
+                    wait_s(&X.v_full[vs], (it / C::V_SLOTS) & 1);
+                    uint8_t *v = sm + C::RING + (C::K_SLOTS + vs) * PF_SLOT_BYTES + tid * 64;        // dim tid of the first tile
                     const int n = there ? kv_end - key0 : 0;
 #pragma unroll 1
                     for (int c = 0; c < 8; ++c) {
@@ -534,11 +595,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&X.p_full[it & 1]);
+                if (lane == 0) mbar_arrive(&X.p_full);
             }
-            op += 2 * nt;
             // ---- the unit's result ----
-            wait(&X.o_done, (it - 1) & 1);
+            wait_s(&X.o_done, (it - 1) & 1);
             tc_fence_after();
             X.red[part][row] = l;
             asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
@@ -666,7 +726,11 @@ template <typename T, int TERMS> cudaError_t launch_prefill_typed(const PfbArgs 
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!ready[dev]) {
-            const cudaError_t e = cudaFuncSetAttribute(block_prefill_kernel<T, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, PfCfg<TERMS>::SMEM);
+            cudaFuncAttributes fa;
+            cudaError_t e = cudaFuncGetAttributes(&fa, block_prefill_kernel<T, TERMS>);
+            if (e != cudaSuccess) return e;
+            if (fa.numRegs != PF_REGS) return cudaErrorInvalidConfiguration;    // setmaxnreg.inc would wait for good
+            e = cudaFuncSetAttribute(block_prefill_kernel<T, TERMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, PfCfg<TERMS>::SMEM);
             if (e != cudaSuccess) return e;
             ready[dev] = true;
         }

@@ -57,7 +57,7 @@ __device__ __forceinline__ void umma_f8_ts(uint32_t d, uint32_t a, uint64_t b, u
 
 #define KVQ_R8(a, o) "r"(a[o]), "r"(a[o + 1]), "r"(a[o + 2]), "r"(a[o + 3]), "r"(a[o + 4]), "r"(a[o + 5]), "r"(a[o + 6]), "r"(a[o + 7])
 #define KVQ_W8(a, o) "=r"(a[o]), "=r"(a[o + 1]), "=r"(a[o + 2]), "=r"(a[o + 3]), "=r"(a[o + 4]), "=r"(a[o + 5]), "=r"(a[o + 6]), "=r"(a[o + 7])
-// Each lane moves 32 (8) consecutive columns of its own TMEM lane; r + at is the first register.
+// Each lane moves 32 (16) consecutive columns of its own TMEM lane; r[AT] is the first register.
 template <int AT, int N> __device__ __forceinline__ void tmem_ld32(uint32_t ta, uint32_t (&r)[N]) {
     static_assert(AT + 32 <= N, "registers");
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
@@ -73,9 +73,11 @@ template <int AT, int N> __device__ __forceinline__ void tmem_st32(uint32_t ta, 
                  KVQ_R8(r, AT), KVQ_R8(r, AT + 8), KVQ_R8(r, AT + 16), KVQ_R8(r, AT + 24)
                  : "memory");
 }
-template <int N> __device__ __forceinline__ void tmem_st8(uint32_t ta, const uint32_t (&r)[N]) {
-    static_assert(N == 8, "registers");
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(ta), KVQ_R8(r, 0) : "memory");
+template <int AT, int N> __device__ __forceinline__ void tmem_st16(uint32_t ta, const uint32_t (&r)[N]) {
+    static_assert(AT + 16 <= N, "registers");
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(ta),
+                 KVQ_R8(r, AT), KVQ_R8(r, AT + 8)
+                 : "memory");
 }
 #undef KVQ_R8
 #undef KVQ_W8
