@@ -66,10 +66,12 @@ int check_pool(const kvq_pool *pool, int layer, PoolGeom *geo) {
     return KVQ_OK;
 }
 
-// Prefill plan: what a row tile costs beyond its steps of 128 keys, in steps, and
-// the shortest part worth a partial result (its merge moves as many bytes as four
-// steps read).
-constexpr int64_t PFB_TILE_COST = 3, PFB_MIN_PART = 4;
+// Prefill plan: what a part of a row tile costs beyond its steps of 128 keys, in
+// steps (its query, its output and the rescaling of its first steps; a 7,777-token
+// prompt took 949, 811, 780 and 765 us planned with 3, 5, 7 and 9, 512 tokens at
+// 32,768 386, 384, 369 and 366), and the shortest part worth a partial result (its
+// merge moves as many bytes as four steps read).
+constexpr int64_t PFB_TILE_COST = 8, PFB_MIN_PART = 4;
 
 int cuda_rc(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ECUDA; }
 
@@ -474,105 +476,86 @@ int kvq_prefill_plan(const kvq_pool_desc *desc, int n_seq, const int32_t *pos0, 
             tiles += n_kv;
         }
     if (tiles > (1 << 24)) return KVQ_EUNSUPPORTED;
-    // Walk the row tiles in order and cut where a CTA's share is used up: the work
-    // that is left over the CTAs that are left, so that what one CTA takes too much
-    // or too little is spread over the later ones.  Parts shorter than PFB_MIN_PART
-    // steps are not made.
-    for (int pass = 0; pass < 2; ++pass) {
-        int64_t units = 0, merges = 0, slots = 0, cta = 0, used = 0, left = total, share = 0;
-        int32_t *U = nullptr, *M = nullptr, *S = nullptr;
-        if (pass == 1) {
-            U = plan + PLAN_HEADER;
-            M = U + (int64_t)info->n_units * PFB_UNIT;
-            S = M + (int64_t)info->n_merges * PFB_MERGE;
-            if (tiles) S[0] = 0;
-        }
-        auto open = [&]() {                // the next CTA's share
-            const int64_t ctas = std::max<int64_t>(n_ctas - cta, 1);
+    if (plan_capacity < 0) return KVQ_EINVAL;
+    // Walk the row tiles in order and cut where a CTA has its share.  Parts shorter
+    // than PFB_MIN_PART steps are not made, and a part costs PFB_TILE_COST whether
+    // it is a whole tile or not, so the share that n_ctas CTAs need is searched for.
+    struct Count {
+        int64_t units = 0, merges = 0, slots = 0, ctas = 0;
+    };
+    auto walk = [&](int64_t share, int32_t *U, int32_t *M, int32_t *S) {
+        Count c;
+        int64_t used = 0, row_start = 0;
+        if (S) S[0] = 0;
+        auto close = [&]() {
+            ++c.ctas;
             used = 0;
-            share = ctas == 1 ? INT64_MAX / 2 : std::max<int64_t>(PFB_MIN_PART + PFB_TILE_COST, (left + ctas - 1) / ctas);
+            if (S) S[c.ctas] = (int32_t)c.units;
         };
-        auto close = [&]() {               // the current CTA ends here
-            ++cta;
-            if (pass == 1) S[cta] = (int32_t)units;
-            open();
-        };
-        open();
-        int64_t row_start = 0;
         for (int b = 0; b < n_seq; ++b) {
             for (int g = 0; g < n_kv; ++g)
                 for (int64_t r0 = 0; r0 < (int64_t)n_tok[b] * G; r0 += PFB_ROWS) {
-                    const int64_t steps = steps_of(b, r0);
-                    const int64_t keys = std::min<int64_t>(n_tok[b], (r0 + PFB_ROWS - 1) / G + 1) + pos0[b];
+                    const int64_t steps = steps_of(b, r0), slot0 = c.slots;
                     int64_t s0 = 0, parts = 0;
-                    const int64_t slot0 = slots;
                     while (s0 < steps) {
-                        const int64_t room = std::max<int64_t>(share - used - PFB_TILE_COST, 0), rest = steps - s0;
-                        int64_t n = rest;
-                        if (room < PFB_MIN_PART && used > 0) {     // nothing worth starting here
+                        const int64_t room = share - used - PFB_TILE_COST, rest = steps - s0;
+                        if (room < PFB_MIN_PART && rest > room && used > 0) {     // nothing worth starting here
                             close();
                             continue;
                         }
-                        if (rest > room + PFB_MIN_PART) n = room;
+                        const int64_t n = rest < room + PFB_MIN_PART ? rest : std::max(room, PFB_MIN_PART);
                         const bool cut = n < rest || s0 > 0;
-                        if (pass == 1) {
-                            int32_t *u = U + units * PFB_UNIT;
-                            u[0] = b;
-                            u[1] = g;
-                            u[2] = (int32_t)r0;
-                            u[3] = (int32_t)(s0 * PFB_KEYS);
-                            u[4] = (int32_t)std::min<int64_t>((s0 + n) * PFB_KEYS, keys);
-                            u[5] = cut ? (int32_t)slots : -1;
-                            u[6] = (int32_t)row_start;
-                            u[7] = pos0[b];
-                            u[8] = n_tok[b];
-                            u[9] = u[10] = u[11] = 0;
+                        if (U) {
+                            const int64_t keys = std::min<int64_t>(n_tok[b], (r0 + PFB_ROWS - 1) / G + 1) + pos0[b];
+                            const int32_t u[PFB_UNIT] = {b, g, (int32_t)r0, (int32_t)(s0 * PFB_KEYS),
+                                                         (int32_t)std::min<int64_t>((s0 + n) * PFB_KEYS, keys),
+                                                         cut ? (int32_t)c.slots : -1, (int32_t)row_start, pos0[b], n_tok[b], 0, 0, 0};
+                            std::copy(u, u + PFB_UNIT, U + c.units * PFB_UNIT);
                         }
-                        ++units;
-                        if (cut) ++slots, ++parts;
+                        ++c.units;
+                        if (cut) ++c.slots, ++parts;
                         s0 += n;
                         used += n + PFB_TILE_COST;
-                        left -= n + (s0 == steps ? PFB_TILE_COST : 0);
                         if (used >= share) close();
                     }
                     if (parts) {
-                        if (pass == 1) {
-                            int32_t *m = M + merges * PFB_MERGE;
-                            m[0] = g;
-                            m[1] = (int32_t)r0;
-                            m[2] = (int32_t)slot0;
-                            m[3] = (int32_t)parts;
-                            m[4] = (int32_t)row_start;
-                            m[5] = n_tok[b];
-                            m[6] = m[7] = 0;
+                        if (M) {
+                            const int32_t m[PFB_MERGE] = {g, (int32_t)r0, (int32_t)slot0, (int32_t)parts, (int32_t)row_start, n_tok[b], 0, 0};
+                            std::copy(m, m + PFB_MERGE, M + c.merges * PFB_MERGE);
                         }
-                        ++merges;
+                        ++c.merges;
                     }
                 }
             row_start += n_tok[b];
         }
         if (used > 0) close();
-        if (pass == 0) {
-            const int64_t len = pfb_plan_len(units, merges, cta);
-            if (len > INT32_MAX) return KVQ_EUNSUPPORTED;
-            info->n_units = (int32_t)units;
-            info->n_ctas = (int32_t)cta;
-            info->n_merges = (int32_t)merges;
-            info->n_slots = (int32_t)slots;
-            info->n_seq = n_seq;
-            info->n_rows = (int32_t)rows;
-            info->n_kv_heads = n_kv;
-            info->group = G;
-            info->plan_len = (int32_t)len;
-            info->reserved = 0;
-            info->workspace_bytes = (uint64_t)slots * PFB_SLOT * sizeof(float);
-            if (!plan || plan_capacity < len) return KVQ_ESIZE;
-            const int32_t head[PLAN_HEADER] = {PFB_MAGIC, (int32_t)units, n_seq, (int32_t)rows, n_kv, G, (int32_t)merges,
-                                               (int32_t)cta};
-            std::copy(head, head + PLAN_HEADER, plan);
-            plan[len - 1] = 0;              // start[0] when there are no CTAs
-        }
+        return c;
+    };
+    int64_t lo = std::max<int64_t>(PFB_MIN_PART + PFB_TILE_COST, (total + n_ctas - 1) / n_ctas), hi = std::max(lo, total);
+    while (lo < hi) {                      // a share of the whole total needs one CTA
+        const int64_t mid = lo + (hi - lo) / (hi > 2 * lo ? 16 : 2);   // the answer is near the mean
+        if (walk(mid, nullptr, nullptr, nullptr).ctas <= n_ctas) hi = mid;
+        else lo = mid + 1;
     }
+    const Count c = walk(lo, nullptr, nullptr, nullptr);
+    const int64_t len = pfb_plan_len(c.units, c.merges, c.ctas);
+    if (len > INT32_MAX) return KVQ_EUNSUPPORTED;
+    info->n_units = (int32_t)c.units;
+    info->n_ctas = (int32_t)c.ctas;
+    info->n_merges = (int32_t)c.merges;
+    info->n_slots = (int32_t)c.slots;
+    info->n_seq = n_seq;
+    info->n_rows = (int32_t)rows;
+    info->n_kv_heads = n_kv;
+    info->group = G;
+    info->plan_len = (int32_t)len;
+    info->reserved = 0;
+    info->workspace_bytes = (uint64_t)c.slots * PFB_SLOT * sizeof(float);
+    if (!plan || plan_capacity < len) return KVQ_ESIZE;
+    const int32_t head[PLAN_HEADER] = {PFB_MAGIC, (int32_t)c.units, n_seq, (int32_t)rows, n_kv, G, (int32_t)c.merges, (int32_t)c.ctas};
+    std::copy(head, head + PLAN_HEADER, plan);
+    int32_t *U = plan + PLAN_HEADER, *M = U + c.units * PFB_UNIT;
+    walk(lo, U, M, M + c.merges * PFB_MERGE);
     return KVQ_OK;
 }
 

@@ -73,10 +73,10 @@ __device__ __forceinline__ bool plan_ok(const PfbArgs &A) {
 // The five 8-bit passes cost 1.25 times two 16-bit ones; what they save is the
 // conversion of every K and V code to 16 bits, which would move as many bytes
 // through shared memory as the products themselves.
-// Weights: W = 2^(s - m) 2^(e_v - E) 2^12, with s the score in base 2, m the row's
+// Weights: W = 2^(s - m) 2^(e_v - E) 2^10, with s the score in base 2, m the row's
 // reference, e_v the exponent of the tile's V scale and E the largest e_v of the
 // unit so far, so V scales cost nothing.  m moves only when a score passes it by
-// 2^3: then, or when E moves, the row's O is multiplied in TMEM.
+// 2^5: then, or when E moves, the row's O is multiplied in TMEM.
 // TMEM: O 0-255, S 256-383, weights 384-479 (term i of the 32 keys c at
 // 384 + 24 c + 8 i); all 512 columns are allocated.  The scores of step j + 1 are
 // made as soon as the softmax has step j's in registers, behind the values of step
@@ -92,6 +92,10 @@ static_assert(2 * PF_REGS_SOFT + PF_REGS_REST <= 3 * PF_REGS, "the softmax warps
 constexpr int PF_SLOT_BYTES = 32768;
 constexpr uint64_t PF_WAIT_NS = 2000000000ull;
 constexpr int PF_S_COL = 256, PF_P_COL = 384;
+// m moves when a score passes it by 2^PF_LAZY; weights are made 2^PF_SHIFT times larger, up to fp16's 2^15.  At 3 and 12 the
+// first steps of a unit rescaled O about twice as often.
+constexpr int PF_LAZY = 5, PF_SHIFT = 10;
+static_assert(PF_LAZY + PF_SHIFT == 15, "the largest weight");
 constexpr int PF_NO_E = -10000;
 
 template <int TERMS> struct PfCfg {
@@ -124,14 +128,27 @@ __device__ __forceinline__ bool pair_any(bool ask, int id) {
     return r != 0;
 }
 
-template <typename T> __device__ __forceinline__ void load_q8(const T *p, float (&x)[8]) {
-    if constexpr (sizeof(T) == 4) {
-        const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    } else {
-        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p));
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+// The 16 query rows of a warp (rows 16 warp .. of the tile, zeros past the last), eight dims a lane.  16-bit rows are
+// held as they are, all 16 loaded at once and a unit ahead of their use; fp32 rows would need twice the registers and
+// are read when they are used.
+__device__ __forceinline__ int64_t query_row(const PfbArgs &A, const Unit &u, int r) {
+    if (r >= u.n_tok * A.G) return -1;
+    const int tok = r / A.G;
+    return (int64_t)(u.row_start + tok) * A.q_stride + (u.head * A.G + r - tok * A.G) * D;
+}
+template <typename T> struct QueryRows {
+    static constexpr bool AHEAD = true;
+    uint4 raw[16];
+    __device__ __forceinline__ void load(const PfbArgs &A, const Unit &u, int warp, int lane) {
+        const int64_t mine = query_row(A, u, u.r0 + 16 * warp + (lane & 15));
+#pragma unroll
+        for (int y = 0; y < 16; ++y) {
+            const int64_t at = __shfl_sync(0xffffffffu, mine, y);
+            raw[y] = at < 0 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(A.q) + at) + lane);
+        }
+    }
+    __device__ __forceinline__ void get(const PfbArgs &, const Unit &, int, int, int y, float (&x)[8]) const {
+        const uint32_t w[4] = {raw[y].x, raw[y].y, raw[y].z, raw[y].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if constexpr (std::is_same_v<T, __half>) {
@@ -144,7 +161,19 @@ template <typename T> __device__ __forceinline__ void load_q8(const T *p, float 
             }
         }
     }
-}
+};
+template <> struct QueryRows<float> {
+    static constexpr bool AHEAD = false;
+    int64_t mine;
+    __device__ __forceinline__ void load(const PfbArgs &A, const Unit &u, int warp, int lane) { mine = query_row(A, u, u.r0 + 16 * warp + (lane & 15)); }
+    __device__ __forceinline__ void get(const PfbArgs &A, const Unit &, int, int lane, int y, float (&x)[8]) const {
+        const int64_t at = __shfl_sync(0xffffffffu, mine, y);
+        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(A.q) + at) + 2 * lane;
+        const float4 a = at < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldg(p), b = at < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldg(p + 1);
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+};
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
@@ -371,7 +400,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PF_REGS_SOFT));
         const int part = warp >> 2, row = 32 * (warp & 3) + lane, bar = 1 + (warp & 3);
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        const T *q = static_cast<const T *>(A.q);
+        QueryRows<T> rows;
         int it = 0;
         auto wait_s = [&](uint64_t *bar, uint32_t parity) {     // as wait, without its answer
             if (!mbar_try_wait(bar, parity)) {
@@ -390,50 +419,36 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
             if (!load_unit(A, i, u)) continue;
             const int n_rows = u.n_tok * A.G, nt = (u.k1 - u.k0 + PFB_KEYS - 1) / PFB_KEYS, kv_end = u.pos0 + u.n_tok;
             // ---- query terms: rows 16 warp .. + 15, eight dims a lane ----
-            int64_t q_row = -1;                          // lane y < 16: where row 16 warp + y of the tile lies in q
-            if (lane < 16 && u.r0 + 16 * warp + lane < n_rows) {
-                const int r = u.r0 + 16 * warp + lane, tok = r / A.G;
-                q_row = (int64_t)(u.row_start + tok) * A.q_stride + (u.head * A.G + r - tok * A.G) * D;
-            }
-#pragma unroll 1
-            for (int yy = 0; yy < 16; yy += 8) {
-                float x[8][8];
+            if (i == i0 || !QueryRows<T>::AHEAD) rows.load(A, u, warp, lane);
 #pragma unroll
-                for (int y = 0; y < 8; ++y) {
-                    const int64_t at = __shfl_sync(0xffffffffu, q_row, yy + y);
-                    if (at >= 0) {
-                        load_q8(q + at + lane * 8, x[y]);
-                    } else {
+            for (int y = 0; y < 16; ++y) {
+                const int r = 16 * warp + y;
+                float x[8];
+                rows.get(A, u, warp, lane, y, x);
+                float mx = 0.0f;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) x[y][e] = 0.0f;
-                    }
-                }
+                for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
+                mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));   // not negative: the bits order as the values
+                const int kq = mx > 0.0f ? max(-114, min(114, 7 - ((int)(__float_as_uint(mx) >> 23) - 127))) : 0;
+                const float up = pow2f(kq);
+                if (lane == 0) X.qscale[r] = pow2f(-kq) * (1.4426950408889634f / 16.0f);
+                // dims 8 lane ..: half lane / 16, chunk (lane / 2) % 8, its low or high 8 bytes
+                uint8_t *dst = sm + (lane >> 4) * 16384 + (r >> 3) * 1024 + (r & 7) * 128 + ((((lane >> 1) & 7) ^ (r & 7)) << 4) + (lane & 1) * 8;
 #pragma unroll
-                for (int y = 0; y < 8; ++y) {
-                    const int r = 16 * warp + yy + y;
-                    float mx = 0.0f;
+                for (int e = 0; e < 8; ++e) x[e] *= up;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[y][e]));
-                    mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));   // not negative: the bits order as the values
-                    const int kq = mx > 0.0f ? max(-114, min(114, 7 - ((int)(__float_as_uint(mx) >> 23) - 127))) : 0;
-                    const float up = pow2f(kq);
-                    if (lane == 0) X.qscale[r] = pow2f(-kq) * (1.4426950408889634f / 16.0f);
-                    // dims 8 lane ..: half lane / 16, chunk (lane / 2) % 8, its low or high 8 bytes
-                    uint8_t *dst = sm + (lane >> 4) * 16384 + (r >> 3) * 1024 + (r & 7) * 128 + ((((lane >> 1) & 7) ^ (r & 7)) << 4) + (lane & 1) * 8;
+                for (int t = 0; t < TERMS; ++t) {
+                    uint32_t w[4];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) x[y][e] *= up;
-#pragma unroll
-                    for (int t = 0; t < TERMS; ++t) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            w[e] = f32x2_to_e4m3x2(x[y][2 * e], x[y][2 * e + 1]);
+                    for (int e = 0; e < 4; ++e) {
+                        w[e] = f32x2_to_e4m3x2(x[2 * e], x[2 * e + 1]);
+                        if (t + 1 < TERMS) {
                             const float2 f = __half22float2(u32_as_h2(e4m3x2_to_h2(w[e])));
-                            x[y][2 * e] -= f.x;
-                            x[y][2 * e + 1] -= f.y;
+                            x[2 * e] -= f.x;
+                            x[2 * e + 1] -= f.y;
                         }
-                        *reinterpret_cast<uint2 *>(dst + t * 32768) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
                     }
+                    *reinterpret_cast<uint2 *>(dst + t * 32768) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
                 }
             }
             fence_async_shared();
@@ -476,7 +491,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
                     top = max(top, E);
                     const int ev = part ? eb : ea;
                     rec_k = part ? sc.z : sc.x;
-                    rec_v = (top << 16) | ((ev == PF_NO_E ? -188 : max(ev - top, -200) + 12) & 0xFFFF);
+                    rec_v = (top << 16) | ((ev == PF_NO_E ? -188 : max(ev - top, -200) + PF_SHIFT) & 0xFFFF);
                     slot = load_slot(step + 32);
                 }
                 if ((j & 31) == 16) sc = load_scales(slot, (j & ~31) + 32 + lane);
@@ -507,7 +522,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
                 for (int x = 0; x < 64; x += 2) mx4[(x >> 1) & 3] = max3(mx4[(x >> 1) & 3], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
                 float mx = max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]);
                 mx *= f;                                                         // f > 0
-                if (pair_any(mx > m + 3.0f || En > E, bar)) {
+                if (pair_any(mx > m + (float)PF_LAZY || En > E, bar)) {
                     X.red[part][row] = mx;
                     asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
                     const float mn = fmaxf(m, fmaxf(X.red[0][row], X.red[1][row]));
@@ -597,6 +612,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&X.p_full);
             }
+            if (QueryRows<T>::AHEAD && i + 1 < i1) {
+                Unit v;
+                if (load_unit(A, i + 1, v)) rows.load(A, v, warp, lane);
+            }
             // ---- the unit's result ----
             wait_s(&X.o_done, (it - 1) & 1);
             tc_fence_after();
@@ -604,7 +623,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
             asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
             l = X.red[0][row] + X.red[1][row];
             const bool cut = u.slot >= 0;
-            const float unit_o = E == PF_NO_E ? 0.0f : exp2f((float)(E - 12));
+            const float unit_o = E == PF_NO_E ? 0.0f : exp2f((float)(E - PF_SHIFT));
             const float fo = cut ? unit_o : (l > 0.0f ? unit_o / l : 0.0f);
             const int tok = r / A.G;
             const int64_t at = r < n_rows ? ((int64_t)(u.row_start + tok) * A.n_q_heads + u.head * A.G + (r - tok * A.G)) * D : -1;

@@ -12,8 +12,8 @@ most w V (2 w V where the sum of weights is not the rounded ones').
    of fp16, 2^-21.  f32: 2 V (2^-15 A + 2^-19).
  prefill: q as two E4M3 terms under a power of two per row holds bf16 exactly down to 2^-10 of a code
    of the row's largest value in [2^7, 2^8), 2^-17 of it; as three terms fp16 and fp32 to 2^-12 besides; weights
-   as three terms of 3 bits, 2^-9, and nothing below 2^-28 of the row's largest
-   (n keys: n 2^-28).  f32: 2 V (2^-15 A + e A + 2^-17 qmax K + 2^-9 + n 2^-28) with e = 0 or 2^-12
+   as three terms of 3 bits, 2^-9, and nothing below 2^-27 of the row's reference (half
+   the smallest E5M2 number, 2^-17, of weights made 2^10 times larger; n keys: n 2^-27).  f32: 2 V (2^-15 A + e A + 2^-17 qmax K + 2^-9 + n 2^-27) with e = 0 or 2^-12
    and K = max_j sum_d |k_jd| / 16.
  bf16: half a step more, 2^-9 of the value.
 """
@@ -431,7 +431,7 @@ def check_prefill(cache, table, pos0, toks, q, out, of, dtype):
             limits = np.repeat(np.arange(p + 1, p + n + 1), G)
             want, a = br.attend(x, k, v, limits)
             V, K = np.abs(v).max(), np.abs(k).sum(1).max() / 16
-            tol = 2 * V * ((2.0 ** -15 + e) * a + 2.0 ** -17 * np.abs(x).max(1) * K + 2.0 ** -9 + (p + n) * 2.0 ** -28)
+            tol = 2 * V * ((2.0 ** -15 + e) * a + 2.0 ** -17 * np.abs(x).max(1) * K + 2.0 ** -9 + (p + n) * 2.0 ** -27)
             got = of[row:row + n, h * G:(h + 1) * G].cpu().numpy().reshape(n * G, 256).astype(np.float64)
             err = np.abs(got - want).max(1)
             assert (err <= tol).all(), f"seq {b} head {h}: row {np.argmax(err / tol)}, {(err / tol).max()} of the tolerance"
