@@ -57,41 +57,47 @@ template <typename T> __device__ __forceinline__ void store_row8(T *row, int lan
     }
 }
 
-// The warp rotates one row at table row cs (rot_dim floats: cosines, sines).
-// rot_dim is a multiple of 16, so a split pair's partner is the same element of
-// another lane, rot_dim / 16 lanes away.
-__device__ __forceinline__ void rope_row(float (&x)[8], const RopeArgs &R, const float *cs, int lane) {
-    const int half = R.rot_dim >> 1;
-    if (R.interleaved) {
-        const bool in = lane * 8 < R.rot_dim;
-        float4 c = make_float4(0.f, 0.f, 0.f, 0.f), s = c;
-        if (in) {
-            c = __ldg(reinterpret_cast<const float4 *>(cs) + lane);
-            s = __ldg(reinterpret_cast<const float4 *>(cs + half) + lane);
+// A position's cosines and sines as the lane needs them: of its four (interleaved)
+// or eight pairs.  rot_dim is a multiple of 16, so a split pair's partner is the
+// same element of another lane, rot_dim / 16 lanes away.
+struct Angles {
+    float c[8], s[8];
+    __device__ __forceinline__ void load(const RopeArgs &R, int pos, int lane) {
+        if (lane * 8 >= R.rot_dim) return;
+        const int half = R.rot_dim >> 1, hl = half >> 3;
+        const float *cs = R.cos_sin + (int64_t)pos * R.rot_dim;
+        if (R.interleaved) {
+            const float4 a = __ldg(reinterpret_cast<const float4 *>(cs) + lane), b = __ldg(reinterpret_cast<const float4 *>(cs + half) + lane);
+            c[0] = a.x; c[1] = a.y; c[2] = a.z; c[3] = a.w;
+            s[0] = b.x; s[1] = b.y; s[2] = b.z; s[3] = b.w;
+        } else {
+            const int at = (lane >= hl ? lane - hl : lane) * 8;
+            load8(cs + at, c);
+            load8(cs + half + at, s);
         }
-        const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-        if (in)
+    }
+};
+
+// The warp rotates one row.
+__device__ __forceinline__ void rope_row(float (&x)[8], const RopeArgs &R, const Angles &a, int lane) {
+    if (R.interleaved) {
+        if (lane * 8 < R.rot_dim)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float a = x[2 * i], b = x[2 * i + 1];
-                x[2 * i] = __fsub_rn(__fmul_rn(a, cc[i]), __fmul_rn(b, ss[i]));
-                x[2 * i + 1] = __fadd_rn(__fmul_rn(b, cc[i]), __fmul_rn(a, ss[i]));
+                const float u = x[2 * i], v = x[2 * i + 1];
+                x[2 * i] = __fsub_rn(__fmul_rn(u, a.c[i]), __fmul_rn(v, a.s[i]));
+                x[2 * i + 1] = __fadd_rn(__fmul_rn(v, a.c[i]), __fmul_rn(u, a.s[i]));
             }
     } else {
-        const int hl = half >> 3;
+        const int hl = R.rot_dim >> 4;
         const bool in = lane < 2 * hl, upper = lane >= hl;
         const int src = in ? (upper ? lane - hl : lane + hl) : lane;
-        float c[8], s[8];
-        if (in) {
-            load8(cs + (upper ? lane - hl : lane) * 8, c);
-            load8(cs + half + (upper ? lane - hl : lane) * 8, s);
-        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float o = __shfl_sync(0xffffffffu, x[i], src);
             if (in)
-                x[i] = upper ? __fadd_rn(__fmul_rn(x[i], c[i]), __fmul_rn(o, s[i]))
-                             : __fsub_rn(__fmul_rn(x[i], c[i]), __fmul_rn(o, s[i]));
+                x[i] = upper ? __fadd_rn(__fmul_rn(x[i], a.c[i]), __fmul_rn(o, a.s[i]))
+                             : __fsub_rn(__fmul_rn(x[i], a.c[i]), __fmul_rn(o, a.s[i]));
         }
     }
 }
@@ -125,7 +131,11 @@ __device__ __forceinline__ void rope_query(const RopeArgs &R, int64_t item, int 
     load_row8<T>(static_cast<const T *>(R.q) + row * R.q_stride + head * D, lane, x);
     int seq, pos;
     if (!row_place(R, row, lane, seq, pos)) return;
-    if (R.rot_dim) rope_row(x, R, R.cos_sin + (int64_t)pos * R.rot_dim, lane);
+    if (R.rot_dim) {
+        Angles a;
+        a.load(R, pos, lane);
+        rope_row(x, R, a, lane);
+    }
     if (FWHT) fwht256_lane(x, lane);
     store_row8<TQ>(static_cast<TQ *>(R.q_out) + (row * R.n_q_heads + head) * D, lane, x);
 }
@@ -152,14 +162,74 @@ __global__ void __launch_bounds__(128) rope_append_kernel(uint8_t *pool, PoolGeo
     const int slot = __ldg(R.page_table + (int64_t)seq * R.max_pages + (pos >> 8));
     uint8_t *tile = token_tile<FMT>(pool, geo, R.layer, slot, head, pos, R.status, lane);
     if (!tile) return;
-    if (R.rot_dim) rope_row(xk, R, R.cos_sin + (int64_t)pos * R.rot_dim, lane);
+    if (R.rot_dim) {
+        Angles a;
+        a.load(R, pos, lane);
+        rope_row(xk, R, a, lane);
+    }
     TokenCodes t;
     quant_token<FMT>(xk, xv, lane, t);
     store_token<FMT>(t, lane, pos & 7, tile);
 }
 
 // ---- fp8b ------------------------------------------------------------------
-constexpr int BA_THREADS = 512;
+constexpr int BA_WARPS = 8, BA_THREADS = BA_WARPS * 32;
+constexpr int BA_ROWS = 8;             // rows of a warp, all loaded before the first is used
+constexpr int64_t BA_FEW = 4736;       // (row, head) items that get a warp each: 148 SMs x 2 CTAs x 8 warps, twice over
+constexpr int BA_DIRECT = 4;           // tokens of a tile up to which their V codes are stored byte by byte
+static_assert(BA_WARPS * BA_ROWS == BT, "a CTA holds a tile's rows");
+
+// Query rows: a warp takes n <= BA_ROWS consecutive (row, head) items, mostly of
+// one or two rows, whose angles it loads once.
+template <typename T, typename TQ> __device__ __forceinline__ void rope_queries(const RopeArgs &R, uint32_t item0, int n, int lane) {
+    const uint32_t n_items = (uint32_t)(R.n_rows * R.n_q_heads), n_q = (uint32_t)R.n_q_heads;   // at most 2^31
+    if (item0 >= n_items) return;
+    n = (int)min((uint32_t)n, n_items - item0);
+    const uint32_t row0 = item0 / n_q, head0 = item0 - row0 * n_q;
+    float x[BA_ROWS][8];
+    {
+        uint32_t h = head0;
+        const T *src = static_cast<const T *>(R.q) + (int64_t)row0 * R.q_stride;
+#pragma unroll
+        for (int y = 0; y < BA_ROWS; ++y) {
+            if (y < n) load_row8<T>(src + h * D, lane, x[y]);
+            if (++h == n_q) h = 0, src += R.q_stride;
+        }
+    }
+    // positions: lane y < n has item y's, -1 where it has none
+    int seq = warp_find_last(R.n_seq, row0, lane, [&](int s) { return (int64_t)__ldg(R.row_start + s); });
+    int pos = -1;
+    if (lane < n) {
+        const int row = (int)((item0 + lane) / n_q);
+        if (row < __ldg(R.row_start + R.n_seq)) {
+            bool found = seq >= 0;
+            while (found && row >= __ldg(R.row_start + seq + 1))
+                if (++seq >= R.n_seq) found = false;
+            if (!found || row < __ldg(R.row_start + seq)) {
+                status_or(R.status, KVQ_STATUS_BAD_PLAN);
+            } else {
+                const int64_t p = (int64_t)__ldg(R.pos0 + seq) + (row - __ldg(R.row_start + seq));
+                if (p < 0 || p >= (int64_t)R.max_pages * PAGE || (R.rot_dim && p >= R.n_pos)) status_or(R.status, KVQ_STATUS_BAD_SLOT);
+                else pos = (int)p;
+            }
+        }
+    }
+    __syncwarp();
+    Angles a;
+    int held = -1;
+    TQ *dst = static_cast<TQ *>(R.q_out) + (int64_t)item0 * D;
+#pragma unroll
+    for (int y = 0; y < BA_ROWS; ++y) {
+        const int p = __shfl_sync(0xffffffffu, pos, y);
+        if (p < 0) continue;
+        if (R.rot_dim) {
+            if (p != held) a.load(R, p, lane);
+            held = p;
+            rope_row(x[y], R, a, lane);
+        }
+        store_row8<TQ>(dst + y * D, lane, x[y]);
+    }
+}
 
 // 16 codes times the power of two f (0 clears them); bytes whose token is not
 // below keep (bit i of keep: byte i is an old token's) stay as they are.
@@ -181,26 +251,27 @@ __device__ __forceinline__ uint4 rescale16(uint4 u, float f, uint32_t keep) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One CTA per (sequence, tile it appends to, KV head); the CTAs after those take
-// the query rows, one warp per (row, head).  Item i belongs to the sequence s
-// whose range [row_start[s] / 64 + 2 s, row_start[s+1] / 64 + 2 (s+1)) holds it:
-// n rows touch at most n / 64 + 2 tiles, so the ranges are found from row_start
-// alone and a surplus item has no rows.  Even warps hold K rows and odd warps V
-// rows, one row's 8 values a lane, up to 8 rows a warp, so the tile's rows are
-// read once and stay in registers between the scale and the codes.
+// One CTA per (sequence, tile it appends to, KV head, K or V); the CTAs after those
+// take the query rows.  Item i belongs to the sequence s whose range
+// [row_start[s] / 64 + 2 s, row_start[s+1] / 64 + 2 (s+1)) holds it: n rows touch
+// at most n / 64 + 2 tiles, so the ranges are found from row_start alone and a
+// surplus item has no rows.  Warp w holds the rows of tokens 8 w .. 8 w + 7 in
+// registers between the tile's scale and its codes, so each row is read once.
+// Bound by HBM for long prompts (K, V and Q once in, codes and Q once out) and by
+// the chain of loads item -> rows and page slot -> scale for a few tokens.
 template <typename T, typename TQ>
-__global__ void __launch_bounds__(BA_THREADS, 1) block_append_kernel(uint8_t *pool, PoolGeom geo, RopeArgs R,
-                                                                     unsigned kv_blocks) {
-    __shared__ float s_max[BA_THREADS / 32];
+__global__ void __launch_bounds__(BA_THREADS, 2) block_append_kernel(uint8_t *pool, PoolGeom geo, RopeArgs R,
+                                                                     unsigned kv_blocks, int q_rows) {
+    __shared__ float s_max[BA_WARPS];
     __shared__ __align__(16) uint8_t s_v[32 * 528];     // V codes: 512 bytes a dim group, 16 of padding
     grid_dependency_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x >= kv_blocks) {
-        rope_query<false, T, TQ>(R, (int64_t)(blockIdx.x - kv_blocks) * (BA_THREADS / 32) + warp, lane);
+        rope_queries<T, TQ>(R, ((blockIdx.x - kv_blocks) * BA_WARPS + warp) * q_rows, q_rows, lane);
         return;
     }
-    const int64_t item = blockIdx.x / geo.n_kv_heads;
-    const int head = (int)(blockIdx.x - item * geo.n_kv_heads);
+    const bool is_v = blockIdx.x & 1;
+    const int item = (blockIdx.x >> 1) / (unsigned)geo.n_kv_heads, head = (int)(blockIdx.x >> 1) - item * geo.n_kv_heads;
     const int seq = warp_find_last(R.n_seq, item, lane, [&](int s) { return (int64_t)(__ldg(R.row_start + s) >> 6) + 2 * (int64_t)s; });
     if (seq < 0) {
         if (threadIdx.x == 0) status_or(R.status, KVQ_STATUS_BAD_PLAN);
@@ -222,33 +293,38 @@ __global__ void __launch_bounds__(BA_THREADS, 1) block_append_kernel(uint8_t *po
     const int64_t tile_i = (int64_t)(p0 >> 6) + (item - ((int64_t)(row0 >> 6) + 2 * (int64_t)seq));
     const int64_t first = tile_i * BT;
     if (first >= end) return;
-    const int t0 = first >= p0 ? 0 : (int)(p0 - first), t1 = (int)min((int64_t)BT, end - first);
     const int slot = __ldg(R.page_table + (int64_t)seq * R.max_pages + (first >> 8));
+    const int t0 = first >= p0 ? 0 : (int)(p0 - first), t1 = (int)min((int64_t)BT, end - first);
+    // the rows; the tile's token 0 would be row rbase (it may lie before row0)
+    const int64_t rbase = row0 + (first - p0);
+    const int tok0 = BA_ROWS * warp;
+    float x[BA_ROWS][8];
+    {
+        const T *src = is_v ? static_cast<const T *>(R.v) : static_cast<const T *>(R.k);
+        const int64_t stride = is_v ? R.v_stride : R.k_stride;
+#pragma unroll
+        for (int i = 0; i < BA_ROWS; ++i)
+            if (tok0 + i >= t0 && tok0 + i < t1) load_row8<T>(src + (rbase + tok0 + i) * stride + head * D, lane, x[i]);
+    }
     if (slot < 0 || slot >= geo.n_pages) {
         if (threadIdx.x == 0) status_or(R.status, KVQ_STATUS_BAD_SLOT);
         return;
     }
     uint8_t *page = pool + R.layer * geo.layer_stride + (int64_t)slot * geo.slot_stride + (int64_t)head * geo.page_bytes;
-    uint8_t *tile = page + (tile_i & 3) * BT_BYTES;
-    float *scale = reinterpret_cast<float *>(page + B_SCALES_OFF) + 2 * (tile_i & 3);
-    const int64_t rbase = row0 + (first - p0);          // the row of the tile's token 0 (may lie before row0)
-    const bool is_v = warp & 1;
-    const float d0 = t0 > 0 ? scale[is_v] : 0.0f;
+    uint8_t *codes = page + (tile_i & 3) * BT_BYTES + (is_v ? BT_K_BYTES : 0);
+    float *scale = reinterpret_cast<float *>(page + B_SCALES_OFF) + 2 * (tile_i & 3) + is_v;
+    const float d0 = t0 > 0 ? *scale : 0.0f;
 
-    // rows: token 8 (warp / 2) + i of the tile, i = 0 .. 7
-    float x[8][8];
     float amax = 0.0f;
     bool odd_value = false;
-    const T *src = is_v ? static_cast<const T *>(R.v) : static_cast<const T *>(R.k);
-    const int64_t stride = is_v ? R.v_stride : R.k_stride;
-    const int tok0 = 8 * (warp >> 1);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (tok0 + i >= t0 && tok0 + i < t1) load_row8<T>(src + (rbase + tok0 + i) * stride + head * D, lane, x[i]);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < BA_ROWS; ++i) {
         if (tok0 + i >= t0 && tok0 + i < t1) {
-            if (!is_v && R.rot_dim) rope_row(x[i], R, R.cos_sin + (first + tok0 + i) * R.rot_dim, lane);
+            if (!is_v && R.rot_dim) {
+                Angles a;
+                a.load(R, (int)first + tok0 + i, lane);
+                rope_row(x[i], R, a, lane);
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 if (!(fabsf(x[i][e]) <= FLT_MAX)) {     // NaN is kept out of the cache, infinity saturates
@@ -259,66 +335,84 @@ __global__ void __launch_bounds__(BA_THREADS, 1) block_append_kernel(uint8_t *po
             }
         }
     }
-#pragma unroll
-    for (int m = 16; m; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));      // not negative: the bits order as the values
     if (__any_sync(0xffffffffu, odd_value) && lane == 0) status_or(R.status, KVQ_STATUS_NONFINITE);
     if (lane == 0) s_max[warp] = amax;
-    __syncthreads();
+    __syncthreads();                                     // also: every thread has read the old scale
 #pragma unroll
-    for (int w = 0; w < BA_THREADS / 64; ++w) amax = fmaxf(amax, s_max[2 * w + is_v]);
+    for (int w = 0; w < BA_WARPS; ++w) amax = fmaxf(amax, s_max[w]);
     const float d = fmaxf(d0, block_scale(amax));
-    if (warp < 2 && lane == 0) scale[is_v] = d;
-
+    if (threadIdx.x == 0) *scale = d;
     const float f = d > 0.0f ? d0 / d : 1.0f;           // exact: both are powers of two (or d0 = 0)
-    const int wi = (warp >> 1) * 32 + lane;              // thread among the 256 of its side
-    const bool whole_v = t0 == 0 && t1 == BT;
+    const float inv = d > 0.0f ? 1.0f / d : 0.0f;        // x * inv is x / d
+    const bool grown = t0 > 0 && f != 1.0f;
+    const bool staged = is_v && (grown || t1 - t0 > BA_DIRECT);
     if (!is_v) {
-        if (t0 > 0 && f != 1.0f)
-            for (int c = wi; c < t0 * 16; c += BA_THREADS / 2) {
-                uint4 *p = reinterpret_cast<uint4 *>(tile + block_k_off(c >> 4, (c & 15) * 16));
+        if (grown)
+            for (int c = threadIdx.x; c < t0 * 16; c += BA_THREADS) {
+                uint4 *p = reinterpret_cast<uint4 *>(codes + block_k_off(c >> 4, (c & 15) * 16));
                 *p = rescale16(*p, f, 0xFFFFu);
             }
-    } else if (!whole_v) {                               // the tile's bytes, rescaled, come to shared memory first
-        for (int c = wi; c < 1024; c += BA_THREADS / 2) {
-            uint4 u = *reinterpret_cast<const uint4 *>(tile + BT_K_BYTES + c * 16);
+    } else if (staged && (t0 > 0 || t1 < BT)) {          // the tile's bytes, rescaled, come to shared memory first
+        for (int c = threadIdx.x; c < 1024; c += BA_THREADS) {
+            uint4 u = reinterpret_cast<const uint4 *>(codes)[c];
             const int row = c >> 2, tok = ((c & 3) ^ ((row >> 1) & 3)) * 16;
-            if (t0 > tok && f != 1.0f) u = rescale16(u, f, t0 - tok >= 16 ? 0xFFFFu : (1u << (t0 - tok)) - 1u);
+            if (grown && t0 > tok) u = rescale16(u, f, t0 - tok >= 16 ? 0xFFFFu : (1u << (t0 - tok)) - 1u);
             *reinterpret_cast<uint4 *>(s_v + (c >> 5) * 528 + (c & 31) * 16) = u;
         }
+        __syncthreads();
     }
-    __syncthreads();
-    const float inv = d > 0.0f ? 1.0f / d : 0.0f;        // a power of two: x * inv is x / d
+    const bool whole = tok0 >= t0 && tok0 + BA_ROWS <= t1;
+    uint32_t c[BA_ROWS][4];                              // two codes a word
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int t = tok0 + i;
-        if (t < t0 || t >= t1) continue;
-        uint32_t c[4];
+    for (int i = 0; i < BA_ROWS; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            c[j] = f32x2_to_e4m3x2(__fmul_rn(x[i][2 * j], inv), __fmul_rn(x[i][2 * j + 1], inv));
-            if (!(d > 0.0f)) c[j] = 0;
+        for (int j = 0; j < 4; ++j)
+            c[i][j] = d > 0.0f ? f32x2_to_e4m3x2(__fmul_rn(x[i][2 * j], inv), __fmul_rn(x[i][2 * j + 1], inv)) : 0u;
+    if (staged && whole) {                               // eight tokens of a dim are eight adjacent bytes
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            uint32_t w[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t sel = e & 1 ? 0x0051u : 0x0040u;
+                w[h] = __byte_perm(__byte_perm(c[4 * h][e >> 1], c[4 * h + 1][e >> 1], sel),
+                                   __byte_perm(c[4 * h + 2][e >> 1], c[4 * h + 3][e >> 1], sel), 0x5410);
+            }
+            *reinterpret_cast<uint2 *>(s_v + lane * 528 + e * 64 + (((warp >> 1) ^ ((e >> 1) & 3)) << 4) + (warp & 1) * 8) = make_uint2(w[0], w[1]);
         }
-        if (!is_v) {
-            *reinterpret_cast<uint2 *>(tile + block_k_off(t, lane * 8)) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-        } else {
+    } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                s_v[lane * 528 + e * 64 + (((t >> 4) ^ ((e >> 1) & 3)) << 4) + (t & 15)] = (uint8_t)(c[e >> 1] >> (8 * (e & 1)));
+        for (int i = 0; i < BA_ROWS; ++i) {
+            const int t = tok0 + i;
+            if (t < t0 || t >= t1) continue;
+            if (!is_v) {
+                *reinterpret_cast<uint2 *>(codes + block_k_off(t, lane * 8)) = make_uint2(c[i][0] | c[i][1] << 16, c[i][2] | c[i][3] << 16);
+            } else {
+                uint8_t *to = staged ? s_v + lane * 528 : codes + lane * 512;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    to[e * 64 + (((t >> 4) ^ ((e >> 1) & 3)) << 4) + (t & 15)] = (uint8_t)(c[i][e >> 1] >> (8 * (e & 1)));
+            }
         }
     }
+    if (!staged) return;
     __syncthreads();
-    for (int c = threadIdx.x; c < 1024; c += BA_THREADS)
-        reinterpret_cast<uint4 *>(tile + BT_K_BYTES)[c] = *reinterpret_cast<const uint4 *>(s_v + (c >> 5) * 528 + (c & 31) * 16);
+    for (int k = threadIdx.x; k < 1024; k += BA_THREADS)
+        reinterpret_cast<uint4 *>(codes)[k] = *reinterpret_cast<const uint4 *>(s_v + (k >> 5) * 528 + (k & 31) * 16);
 }
 
 template <typename T, typename TQ>
 cudaError_t launch_typed(int fmt, uint8_t *pool, const PoolGeom &geo, const RopeArgs &R, cudaStream_t s) {
     const int64_t q_items = R.q ? R.n_rows * R.n_q_heads : 0;
     if (fmt == KVQ_FP8B) {
-        const int64_t kv = R.k ? ((R.n_rows >> 6) + 2 * (int64_t)R.n_seq) * geo.n_kv_heads : 0;
-        const int64_t qb = (q_items + BA_THREADS / 32 - 1) / (BA_THREADS / 32);
+        const int64_t kv = R.k ? ((R.n_rows >> 6) + 2 * (int64_t)R.n_seq) * geo.n_kv_heads * 2 : 0;
+        // a few query rows are spread over as many warps; many are taken BA_ROWS at a time, for the loads in flight and
+        // the angles they share
+        const int q_rows = q_items <= BA_FEW ? 1 : BA_ROWS;
+        const int64_t qb = (q_items + BA_WARPS * q_rows - 1) / (BA_WARPS * q_rows);
         return launch_ex(block_append_kernel<T, TQ>, dim3((unsigned)(kv + qb)), dim3(BA_THREADS), 0, s, false, pool, geo,
-                         R, (unsigned)kv);
+                         R, (unsigned)kv, q_rows);
     }
     if constexpr (std::is_same_v<TQ, float>) {           // the decodes of these formats take fp32 queries
         const int64_t kv = R.k ? (R.n_rows * geo.n_kv_heads + 3) / 4 : 0, qb = (q_items + 3) / 4;
