@@ -58,8 +58,9 @@ template <typename T> __device__ __forceinline__ void store_row8(T *row, int lan
 }
 
 // A position's cosines and sines as the lane needs them: of its four (interleaved)
-// or eight pairs.  rot_dim is a multiple of 16, so a split pair's partner is the
-// same element of another lane, rot_dim / 16 lanes away.
+// or eight pairs, the sine negated where it is subtracted (a c - b s and
+// a c + b (-s) are the same roundings).  rot_dim is a multiple of 16, so a split
+// pair's partner is the same element of another lane, rot_dim / 16 lanes away.
 struct Angles {
     float c[8], s[8];
     __device__ __forceinline__ void load(const RopeArgs &R, int pos, int lane) {
@@ -74,6 +75,9 @@ struct Angles {
             const int at = (lane >= hl ? lane - hl : lane) * 8;
             load8(cs + at, c);
             load8(cs + half + at, s);
+            if (lane < hl)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[i] = -s[i];
         }
     }
 };
@@ -90,15 +94,14 @@ __device__ __forceinline__ void rope_row(float (&x)[8], const RopeArgs &R, const
             }
     } else {
         const int hl = R.rot_dim >> 4;
-        const bool in = lane < 2 * hl, upper = lane >= hl;
-        const int src = in ? (upper ? lane - hl : lane + hl) : lane;
+        const bool in = lane < 2 * hl;
+        const int src = in ? (lane >= hl ? lane - hl : lane + hl) : lane;
+        float o[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float o = __shfl_sync(0xffffffffu, x[i], src);
-            if (in)
-                x[i] = upper ? __fadd_rn(__fmul_rn(x[i], a.c[i]), __fmul_rn(o, a.s[i]))
-                             : __fsub_rn(__fmul_rn(x[i], a.c[i]), __fmul_rn(o, a.s[i]));
-        }
+        for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, x[i], src);
+        if (in)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __fadd_rn(__fmul_rn(x[i], a.c[i]), __fmul_rn(o[i], a.s[i]));
     }
 }
 
@@ -173,11 +176,11 @@ __global__ void __launch_bounds__(128) rope_append_kernel(uint8_t *pool, PoolGeo
 }
 
 // ---- fp8b ------------------------------------------------------------------
-constexpr int BA_WARPS = 8, BA_THREADS = BA_WARPS * 32;
-constexpr int BA_ROWS = 8;             // rows of a warp, all loaded before the first is used
-constexpr int64_t BA_FEW = 4736;       // (row, head) items that get a warp each: 148 SMs x 2 CTAs x 8 warps, twice over
+constexpr int BA_WARPS = 16, BA_THREADS = BA_WARPS * 32;
+constexpr int BA_ROWS = 4;             // rows of a warp, all loaded before the first is used
+constexpr int64_t BA_FEW = 4736;       // (row, head) items that get a warp each: 148 SMs x 2 CTAs x 16 warps
 constexpr int BA_DIRECT = 4;           // tokens of a tile up to which their V codes are stored byte by byte
-static_assert(BA_WARPS * BA_ROWS == BT, "a CTA holds a tile's rows");
+static_assert(BA_WARPS * BA_ROWS == BT && BA_ROWS == 4, "a CTA holds a tile's rows, a warp the tokens of one word of V codes");
 
 // Query rows: a warp takes n <= BA_ROWS consecutive (row, head) items, mostly of
 // one or two rows, whose angles it loads once.
@@ -255,7 +258,7 @@ __device__ __forceinline__ uint4 rescale16(uint4 u, float f, uint32_t keep) {
 // take the query rows.  Item i belongs to the sequence s whose range
 // [row_start[s] / 64 + 2 s, row_start[s+1] / 64 + 2 (s+1)) holds it: n rows touch
 // at most n / 64 + 2 tiles, so the ranges are found from row_start alone and a
-// surplus item has no rows.  Warp w holds the rows of tokens 8 w .. 8 w + 7 in
+// surplus item has no rows.  Warp w holds the rows of tokens 4 w .. 4 w + 3 in
 // registers between the tile's scale and its codes, so each row is read once.
 // Bound by HBM for long prompts (K, V and Q once in, codes and Q once out) and by
 // the chain of loads item -> rows and page slot -> scale for a few tokens.
@@ -315,8 +318,7 @@ __global__ void __launch_bounds__(BA_THREADS, 2) block_append_kernel(uint8_t *po
     float *scale = reinterpret_cast<float *>(page + B_SCALES_OFF) + 2 * (tile_i & 3) + is_v;
     const float d0 = t0 > 0 ? *scale : 0.0f;
 
-    float amax = 0.0f;
-    bool odd_value = false;
+    float amax = 0.0f, odd = 0.0f;                       // odd: NaN once a value is not finite
 #pragma unroll
     for (int i = 0; i < BA_ROWS; ++i) {
         if (tok0 + i >= t0 && tok0 + i < t1) {
@@ -327,16 +329,24 @@ __global__ void __launch_bounds__(BA_THREADS, 2) block_append_kernel(uint8_t *po
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                if (!(fabsf(x[i][e]) <= FLT_MAX)) {     // NaN is kept out of the cache, infinity saturates
-                    odd_value = true;
-                    x[i][e] = x[i][e] != x[i][e] ? 0.0f : copysignf(FLT_MAX, x[i][e]);
-                }
                 amax = fmaxf(amax, fabsf(x[i][e]));
+                odd = fmaf(x[i][e], 0.0f, odd);
             }
         }
     }
+    if (__any_sync(0xffffffffu, odd != 0.0f)) {          // NaN is kept out of the cache, infinity saturates
+        if (lane == 0) status_or(R.status, KVQ_STATUS_NONFINITE);
+        amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < BA_ROWS; ++i)
+            if (tok0 + i >= t0 && tok0 + i < t1)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (!(fabsf(x[i][e]) <= FLT_MAX)) x[i][e] = x[i][e] != x[i][e] ? 0.0f : copysignf(FLT_MAX, x[i][e]);
+                    amax = fmaxf(amax, fabsf(x[i][e]));
+                }
+    }
     amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));      // not negative: the bits order as the values
-    if (__any_sync(0xffffffffu, odd_value) && lane == 0) status_or(R.status, KVQ_STATUS_NONFINITE);
     if (lane == 0) s_max[warp] = amax;
     __syncthreads();                                     // also: every thread has read the old scale
 #pragma unroll
@@ -369,17 +379,12 @@ __global__ void __launch_bounds__(BA_THREADS, 2) block_append_kernel(uint8_t *po
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             c[i][j] = d > 0.0f ? f32x2_to_e4m3x2(__fmul_rn(x[i][2 * j], inv), __fmul_rn(x[i][2 * j + 1], inv)) : 0u;
-    if (staged && whole) {                               // eight tokens of a dim are eight adjacent bytes
+    if (staged && whole) {                               // the warp's tokens of a dim are adjacent bytes
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            uint32_t w[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t sel = e & 1 ? 0x0051u : 0x0040u;
-                w[h] = __byte_perm(__byte_perm(c[4 * h][e >> 1], c[4 * h + 1][e >> 1], sel),
-                                   __byte_perm(c[4 * h + 2][e >> 1], c[4 * h + 3][e >> 1], sel), 0x5410);
-            }
-            *reinterpret_cast<uint2 *>(s_v + lane * 528 + e * 64 + (((warp >> 1) ^ ((e >> 1) & 3)) << 4) + (warp & 1) * 8) = make_uint2(w[0], w[1]);
+            const uint32_t sel = e & 1 ? 0x0051u : 0x0040u;
+            const uint32_t w = __byte_perm(__byte_perm(c[0][e >> 1], c[1][e >> 1], sel), __byte_perm(c[2][e >> 1], c[3][e >> 1], sel), 0x5410);
+            *reinterpret_cast<uint32_t *>(s_v + lane * 528 + e * 64 + (((warp >> 2) ^ ((e >> 1) & 3)) << 4) + (warp & 3) * 4) = w;
         }
     } else {
 #pragma unroll
