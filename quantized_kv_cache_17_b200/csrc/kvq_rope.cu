@@ -182,6 +182,138 @@ constexpr int64_t BA_FEW = 4736;       // (row, head) items that get a warp each
 constexpr int BA_DIRECT = 4;           // tokens of a tile up to which their V codes are stored byte by byte
 static_assert(BA_WARPS * BA_ROWS == BT && BA_ROWS == 4, "a CTA holds a tile's rows, a warp the tokens of one word of V codes");
 
+// Which eight dims of a row a lane holds: a .. a + 3 and b .. b + 3.  With split
+// pairs the lanes of the rotated part hold both halves of their pairs, so nothing
+// moves between lanes; everywhere else the eight are adjacent.
+struct Dims {
+    int a, b;
+    bool split;                        // of the warp: not all lanes' dims are adjacent
+    bool turns;                        // this lane's dims are rotated
+    __device__ __forceinline__ Dims(int rot_dim, int interleaved, int lane) {
+        const int half = rot_dim >> 1;
+        split = rot_dim > 0 && !interleaved;
+        turns = split ? lane < (half >> 2) : lane * 8 < rot_dim;
+        a = split ? (turns ? 4 * lane : rot_dim + 8 * (lane - (half >> 2))) : 8 * lane;
+        b = split && turns ? half + 4 * lane : a + 4;
+    }
+};
+
+__device__ __forceinline__ void unpack4(const uint2 &u, float *x, __nv_bfloat16) {
+    x[0] = __uint_as_float(u.x << 16);
+    x[1] = __uint_as_float(u.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(u.y << 16);
+    x[3] = __uint_as_float(u.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void unpack4(const uint2 &u, float *x, __half) {
+    const float2 p = __half22float2(u32_as_h2(u.x)), q = __half22float2(u32_as_h2(u.y));
+    x[0] = p.x;
+    x[1] = p.y;
+    x[2] = q.x;
+    x[3] = q.y;
+}
+
+// A row's eight values as they are in memory.
+template <typename T> struct Raw {
+    uint2 a, b;
+    __device__ __forceinline__ void load(const T *row, const Dims &m) {
+        if (m.split) {
+            a = __ldg(reinterpret_cast<const uint2 *>(row + m.a));
+            b = __ldg(reinterpret_cast<const uint2 *>(row + m.b));
+        } else {
+            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(row + m.a));
+            a = make_uint2(u.x, u.y);
+            b = make_uint2(u.z, u.w);
+        }
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        unpack4(a, x, T{});
+        unpack4(b, x + 4, T{});
+    }
+};
+template <> struct Raw<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *row, const Dims &m) {
+        a = __ldg(reinterpret_cast<const float4 *>(row + m.a));
+        b = __ldg(reinterpret_cast<const float4 *>(row + m.b));
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+};
+
+template <typename TQ> __device__ __forceinline__ void store_dims(TQ *row, const Dims &m, const float (&x)[8]) {
+    if constexpr (sizeof(TQ) == 4) {
+        *reinterpret_cast<float4 *>(row + m.a) = make_float4(x[0], x[1], x[2], x[3]);
+        *reinterpret_cast<float4 *>(row + m.b) = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+        const uint2 u = make_uint2(pack2(x[0], x[1], TQ{}), pack2(x[2], x[3], TQ{})), v = make_uint2(pack2(x[4], x[5], TQ{}), pack2(x[6], x[7], TQ{}));
+        if (m.split) {
+            *reinterpret_cast<uint2 *>(row + m.a) = u;
+            *reinterpret_cast<uint2 *>(row + m.b) = v;
+        } else {
+            *reinterpret_cast<uint4 *>(row + m.a) = make_uint4(u.x, u.y, v.x, v.y);
+        }
+    }
+}
+
+// Two fp32 values in one 64-bit register, one instruction for both, each result
+// rounded once.
+__device__ __forceinline__ uint64_t f2(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ void un2(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// The sums of two products each, added one by one: an add.rn.f32x2 of two
+// mul.rn.f32x2 came out fused, rounded once (the last bit of q differed).
+__device__ __forceinline__ void sum2(uint64_t a, uint64_t b, float &x, float &y) {
+    float a0, a1, b0, b1;
+    un2(a, a0, a1);
+    un2(b, b0, b1);
+    x = __fadd_rn(a0, b0);
+    y = __fadd_rn(a1, b1);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// The cosines and sines of a lane's four pairs at one position.
+struct Turn {
+    float4 c, s;
+    __device__ __forceinline__ void load(const RopeArgs &R, int pos, int lane, const Dims &m) {
+        if (!m.turns) return;
+        const float *cs = R.cos_sin + (int64_t)pos * R.rot_dim + 4 * lane;
+        c = __ldg(reinterpret_cast<const float4 *>(cs));
+        s = __ldg(reinterpret_cast<const float4 *>(cs + (R.rot_dim >> 1)));
+    }
+    // a c - b s as a c + b (-s): the same roundings
+    __device__ __forceinline__ void apply(float (&x)[8], const Dims &m) const {
+        if (!m.turns) return;
+        const uint64_t c0 = f2(c.x, c.y), c1 = f2(c.z, c.w), s0 = f2(s.x, s.y), s1 = f2(s.z, s.w), n0 = f2(-s.x, -s.y), n1 = f2(-s.z, -s.w);
+        if (m.split) {
+            const uint64_t a0 = f2(x[0], x[1]), a1 = f2(x[2], x[3]), b0 = f2(x[4], x[5]), b1 = f2(x[6], x[7]);
+            sum2(mul2(a0, c0), mul2(b0, n0), x[0], x[1]);
+            sum2(mul2(a1, c1), mul2(b1, n1), x[2], x[3]);
+            sum2(mul2(b0, c0), mul2(a0, s0), x[4], x[5]);
+            sum2(mul2(b1, c1), mul2(a1, s1), x[6], x[7]);
+        } else {
+            const uint64_t a0 = f2(x[0], x[2]), a1 = f2(x[4], x[6]), b0 = f2(x[1], x[3]), b1 = f2(x[5], x[7]);
+            sum2(mul2(a0, c0), mul2(b0, n0), x[0], x[2]);
+            sum2(mul2(a1, c1), mul2(b1, n1), x[4], x[6]);
+            sum2(mul2(b0, c0), mul2(a0, s0), x[1], x[3]);
+            sum2(mul2(b1, c1), mul2(a1, s1), x[5], x[7]);
+        }
+    }
+};
+
 // Query rows: a warp takes n <= BA_ROWS consecutive (row, head) items, mostly of
 // one or two rows, whose angles it loads once.
 template <typename T, typename TQ> __device__ __forceinline__ void rope_queries(const RopeArgs &R, uint32_t item0, int n, int lane) {
@@ -189,13 +321,14 @@ template <typename T, typename TQ> __device__ __forceinline__ void rope_queries(
     if (item0 >= n_items) return;
     n = (int)min((uint32_t)n, n_items - item0);
     const uint32_t row0 = item0 / n_q, head0 = item0 - row0 * n_q;
-    float x[BA_ROWS][8];
+    const Dims m(R.rot_dim, R.interleaved, lane);
+    Raw<T> raw[BA_ROWS];
     {
         uint32_t h = head0;
         const T *src = static_cast<const T *>(R.q) + (int64_t)row0 * R.q_stride;
 #pragma unroll
         for (int y = 0; y < BA_ROWS; ++y) {
-            if (y < n) load_row8<T>(src + h * D, lane, x[y]);
+            if (y < n) raw[y].load(src + h * D, m);
             if (++h == n_q) h = 0, src += R.q_stride;
         }
     }
@@ -218,19 +351,21 @@ template <typename T, typename TQ> __device__ __forceinline__ void rope_queries(
         }
     }
     __syncwarp();
-    Angles a;
+    Turn turn;
     int held = -1;
     TQ *dst = static_cast<TQ *>(R.q_out) + (int64_t)item0 * D;
 #pragma unroll
     for (int y = 0; y < BA_ROWS; ++y) {
         const int p = __shfl_sync(0xffffffffu, pos, y);
         if (p < 0) continue;
+        float x[8];
+        raw[y].get(x);
         if (R.rot_dim) {
-            if (p != held) a.load(R, p, lane);
+            if (p != held) turn.load(R, p, lane, m);
             held = p;
-            rope_row(x[y], R, a, lane);
+            turn.apply(x, m);
         }
-        store_row8<TQ>(dst + y * D, lane, x[y]);
+        store_dims<TQ>(dst + y * D, m, x);
     }
 }
 
@@ -258,13 +393,15 @@ __device__ __forceinline__ uint4 rescale16(uint4 u, float f, uint32_t keep) {
 // take the query rows.  Item i belongs to the sequence s whose range
 // [row_start[s] / 64 + 2 s, row_start[s+1] / 64 + 2 (s+1)) holds it: n rows touch
 // at most n / 64 + 2 tiles, so the ranges are found from row_start alone and a
-// surplus item has no rows.  Warp w holds the rows of tokens 4 w .. 4 w + 3 in
+// surplus item has no rows.  Where the rows are fewer than those items (by_row:
+// decoding batches), item i is row i, and a tile is taken by its first row.
+// Warp w holds the rows of tokens 4 w .. 4 w + 3 in
 // registers between the tile's scale and its codes, so each row is read once.
 // Bound by HBM for long prompts (K, V and Q once in, codes and Q once out) and by
 // the chain of loads item -> rows and page slot -> scale for a few tokens.
 template <typename T, typename TQ>
 __global__ void __launch_bounds__(BA_THREADS, 2) block_append_kernel(uint8_t *pool, PoolGeom geo, RopeArgs R,
-                                                                     unsigned kv_blocks, int q_rows) {
+                                                                     unsigned kv_blocks, int by_row, int q_rows) {
     __shared__ float s_max[BA_WARPS];
     __shared__ __align__(16) uint8_t s_v[32 * 528];     // V codes: 512 bytes a dim group, 16 of padding
     grid_dependency_wait();
@@ -275,7 +412,8 @@ __global__ void __launch_bounds__(BA_THREADS, 2) block_append_kernel(uint8_t *po
     }
     const bool is_v = blockIdx.x & 1;
     const int item = (blockIdx.x >> 1) / (unsigned)geo.n_kv_heads, head = (int)(blockIdx.x >> 1) - item * geo.n_kv_heads;
-    const int seq = warp_find_last(R.n_seq, item, lane, [&](int s) { return (int64_t)(__ldg(R.row_start + s) >> 6) + 2 * (int64_t)s; });
+    const int seq = by_row ? warp_find_last(R.n_seq, item, lane, [&](int s) { return (int64_t)__ldg(R.row_start + s); })
+                           : warp_find_last(R.n_seq, item, lane, [&](int s) { return (int64_t)(__ldg(R.row_start + s) >> 6) + 2 * (int64_t)s; });
     if (seq < 0) {
         if (threadIdx.x == 0) status_or(R.status, KVQ_STATUS_BAD_PLAN);
         return;
@@ -285,7 +423,7 @@ __global__ void __launch_bounds__(BA_THREADS, 2) block_append_kernel(uint8_t *po
         if (threadIdx.x == 0) status_or(R.status, KVQ_STATUS_BAD_PLAN);
         return;
     }
-    if (row1 == row0) return;
+    if (by_row ? item >= row1 : row1 == row0) return;    // padding, or no rows
     int64_t end = (int64_t)p0 + (row1 - row0);
     const int64_t room = R.rot_dim ? min((int64_t)R.max_pages * PAGE, (int64_t)R.n_pos) : (int64_t)R.max_pages * PAGE;
     if (p0 < 0 || end > room) {
@@ -293,21 +431,25 @@ __global__ void __launch_bounds__(BA_THREADS, 2) block_append_kernel(uint8_t *po
         if (p0 < 0) return;
         end = min(end, room);
     }
-    const int64_t tile_i = (int64_t)(p0 >> 6) + (item - ((int64_t)(row0 >> 6) + 2 * (int64_t)seq));
+    const int64_t tile_i = by_row ? ((int64_t)p0 + (item - row0)) >> 6
+                                  : (int64_t)(p0 >> 6) + (item - ((int64_t)(row0 >> 6) + 2 * (int64_t)seq));
     const int64_t first = tile_i * BT;
     if (first >= end) return;
+    if (by_row && item > row0 && (int64_t)p0 + (item - row0) != first) return;   // not the tile's first row
     const int slot = __ldg(R.page_table + (int64_t)seq * R.max_pages + (first >> 8));
     const int t0 = first >= p0 ? 0 : (int)(p0 - first), t1 = (int)min((int64_t)BT, end - first);
     // the rows; the tile's token 0 would be row rbase (it may lie before row0)
     const int64_t rbase = row0 + (first - p0);
     const int tok0 = BA_ROWS * warp;
+    const Dims m(is_v ? 0 : R.rot_dim, R.interleaved, lane);
+    Raw<T> raw[BA_ROWS];
     float x[BA_ROWS][8];
     {
         const T *src = is_v ? static_cast<const T *>(R.v) : static_cast<const T *>(R.k);
         const int64_t stride = is_v ? R.v_stride : R.k_stride;
 #pragma unroll
         for (int i = 0; i < BA_ROWS; ++i)
-            if (tok0 + i >= t0 && tok0 + i < t1) load_row8<T>(src + (rbase + tok0 + i) * stride + head * D, lane, x[i]);
+            if (tok0 + i >= t0 && tok0 + i < t1) raw[i].load(src + (rbase + tok0 + i) * stride + head * D, m);
     }
     if (slot < 0 || slot >= geo.n_pages) {
         if (threadIdx.x == 0) status_or(R.status, KVQ_STATUS_BAD_SLOT);
@@ -318,23 +460,27 @@ __global__ void __launch_bounds__(BA_THREADS, 2) block_append_kernel(uint8_t *po
     float *scale = reinterpret_cast<float *>(page + B_SCALES_OFF) + 2 * (tile_i & 3) + is_v;
     const float d0 = t0 > 0 ? *scale : 0.0f;
 
-    float amax = 0.0f, odd = 0.0f;                       // odd: NaN once a value is not finite
+    float amax = 0.0f;
+    uint64_t odd2 = 0;                                   // NaN once a value is not finite
 #pragma unroll
     for (int i = 0; i < BA_ROWS; ++i) {
         if (tok0 + i >= t0 && tok0 + i < t1) {
+            raw[i].get(x[i]);
             if (!is_v && R.rot_dim) {
-                Angles a;
-                a.load(R, (int)first + tok0 + i, lane);
-                rope_row(x[i], R, a, lane);
+                Turn turn;
+                turn.load(R, (int)first + tok0 + i, lane, m);
+                turn.apply(x[i], m);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                amax = fmaxf(amax, fabsf(x[i][e]));
-                odd = fmaf(x[i][e], 0.0f, odd);
+            for (int e = 0; e < 8; e += 2) {
+                asm("max.f32 %0, %1, %2, %3;" : "=f"(amax) : "f"(amax), "f"(fabsf(x[i][e])), "f"(fabsf(x[i][e + 1])));
+                odd2 = fma2(f2(x[i][e], x[i][e + 1]), 0, odd2);
             }
         }
     }
-    if (__any_sync(0xffffffffu, odd != 0.0f)) {          // NaN is kept out of the cache, infinity saturates
+    float odd, odd1;
+    un2(odd2, odd, odd1);
+    if (__any_sync(0xffffffffu, odd + odd1 != 0.0f)) {   // NaN is kept out of the cache, infinity saturates
         if (lane == 0) status_or(R.status, KVQ_STATUS_NONFINITE);
         amax = 0.0f;
 #pragma unroll
@@ -374,11 +520,18 @@ __global__ void __launch_bounds__(BA_THREADS, 2) block_append_kernel(uint8_t *po
     }
     const bool whole = tok0 >= t0 && tok0 + BA_ROWS <= t1;
     uint32_t c[BA_ROWS][4];                              // two codes a word
+    const uint64_t inv2 = f2(inv, inv);
 #pragma unroll
     for (int i = 0; i < BA_ROWS; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            c[i][j] = d > 0.0f ? f32x2_to_e4m3x2(__fmul_rn(x[i][2 * j], inv), __fmul_rn(x[i][2 * j + 1], inv)) : 0u;
+        for (int j = 0; j < 4; ++j) {
+            float lo, hi;
+            un2(mul2(f2(x[i][2 * j], x[i][2 * j + 1]), inv2), lo, hi);
+            c[i][j] = f32x2_to_e4m3x2(lo, hi);
+        }
+    if (!(d > 0.0f))                                     // all values are 0, some of them perhaps -0
+#pragma unroll
+        for (int i = 0; i < BA_ROWS; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0;
     if (staged && whole) {                               // the warp's tokens of a dim are adjacent bytes
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -392,7 +545,8 @@ __global__ void __launch_bounds__(BA_THREADS, 2) block_append_kernel(uint8_t *po
             const int t = tok0 + i;
             if (t < t0 || t >= t1) continue;
             if (!is_v) {
-                *reinterpret_cast<uint2 *>(codes + block_k_off(t, lane * 8)) = make_uint2(c[i][0] | c[i][1] << 16, c[i][2] | c[i][3] << 16);
+                *reinterpret_cast<uint32_t *>(codes + block_k_off(t, m.a)) = c[i][0] | c[i][1] << 16;
+                *reinterpret_cast<uint32_t *>(codes + block_k_off(t, m.b)) = c[i][2] | c[i][3] << 16;
             } else {
                 uint8_t *to = staged ? s_v + lane * 528 : codes + lane * 512;
 #pragma unroll
@@ -411,13 +565,15 @@ template <typename T, typename TQ>
 cudaError_t launch_typed(int fmt, uint8_t *pool, const PoolGeom &geo, const RopeArgs &R, cudaStream_t s) {
     const int64_t q_items = R.q ? R.n_rows * R.n_q_heads : 0;
     if (fmt == KVQ_FP8B) {
-        const int64_t kv = R.k ? ((R.n_rows >> 6) + 2 * (int64_t)R.n_seq) * geo.n_kv_heads * 2 : 0;
+        const int64_t by_tiles = (R.n_rows >> 6) + 2 * (int64_t)R.n_seq;
+        const int by_row = R.n_rows < by_tiles ? 1 : 0;
+        const int64_t kv = R.k ? (by_row ? R.n_rows : by_tiles) * geo.n_kv_heads * 2 : 0;
         // a few query rows are spread over as many warps; many are taken BA_ROWS at a time, for the loads in flight and
         // the angles they share
         const int q_rows = q_items <= BA_FEW ? 1 : BA_ROWS;
         const int64_t qb = (q_items + BA_WARPS * q_rows - 1) / (BA_WARPS * q_rows);
         return launch_ex(block_append_kernel<T, TQ>, dim3((unsigned)(kv + qb)), dim3(BA_THREADS), 0, s, false, pool, geo,
-                         R, (unsigned)kv, q_rows);
+                         R, (unsigned)kv, by_row, q_rows);
     }
     if constexpr (std::is_same_v<TQ, float>) {           // the decodes of these formats take fp32 queries
         const int64_t kv = R.k ? (R.n_rows * geo.n_kv_heads + 3) / 4 : 0, qb = (q_items + 3) / 4;
