@@ -143,6 +143,8 @@ def _ptr(t) -> Optional[int]:
 def _stream(stream) -> Optional[int]:
     if stream is None:
         import torch
+        if torch.cuda.is_initialized():              # the same handle, without building a Stream object (3 us a call)
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -322,21 +324,37 @@ def paged_decode_attn_fp8b(pool, layer, q, page_table, plan_dev, info, workspace
 
 
 def _dtype(t, what: str) -> int:
-    """The kvq_dtype of a tensor's elements."""
+    """The kvq_dtype of a torch element type."""
     import torch
-    try:
-        return {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}[t]
-    except KeyError:
-        raise KVQError(f"{what}: {t} is not float32, bfloat16 or float16") from None
+    d = 0 if t is torch.float32 else 1 if t is torch.bfloat16 else 2 if t is torch.float16 else None
+    if d is None:
+        raise KVQError(f"{what}: {t} is not float32, bfloat16 or float16")
+    return d
 
 
 def _rows(t, heads: int, what: str) -> int:
     """The row stride, in elements, of a [rows, heads, 256] tensor whose heads lie side by side in a row."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != HEAD_DIM or t.stride(2) != 1 or \
-            (heads > 1 and t.stride(1) != HEAD_DIM):
-        raise KVQError(f"{what}: want [rows, {heads}, {HEAD_DIM}] with contiguous rows, got {tuple(t.shape)} with "
-                       f"strides {tuple(t.stride())}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), heads * HEAD_DIM)
+    sh, st = t.shape, t.stride()
+    if len(sh) != 3 or sh[1] != heads or sh[2] != HEAD_DIM or st[2] != 1 or (heads > 1 and st[1] != HEAD_DIM):
+        raise KVQError(f"{what}: want [rows, {heads}, {HEAD_DIM}] with contiguous rows, got {tuple(sh)} with strides {st}")
+    return st[0] if sh[0] > 1 else heads * HEAD_DIM + (-heads * HEAD_DIM % 8)
+
+
+def _index(t, what: str) -> int:
+    """Address of a contiguous int32 tensor."""
+    import torch
+    if t.dtype is not torch.int32 or not t.is_contiguous():
+        raise KVQError(f"{what} is not a contiguous int32 tensor")
+    return t.data_ptr()
+
+
+def _on_current_device(what: str, *tensors):
+    """The kernels are launched on the current device: every tensor of the call has to be there."""
+    import torch
+    dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise KVQError(f"{what}: a tensor is on {t.device}, the current device is cuda:{dev}")
 
 
 def kv_append_rope(pool: KVPool, layer: int, k, v, row_start, pos0, page_table, cos_sin=None, interleaved=False, q=None,
@@ -348,41 +366,48 @@ def kv_append_rope(pool: KVPool, layer: int, k, v, row_start, pos0, page_table, 
     row_start[s] .. row_start[s+1] - 1 at positions pos0[s] ..; row_start, pos0 and
     page_table are device int32.  Returns the rotated q (q_out, or a new tensor of
     type q_out_dtype: fp32, or q's own type for fp8b pools; by default fp32 except
-    that fp8b keeps q's type), None without q.  k and v may both be None."""
+    that fp8b keeps q's type; rows past row_start[-1] are not written), None without
+    q.  k and v may both be None."""
     import torch
     d = pool.desc
     first = k if k is not None else q
     if first is None or (k is None) != (v is None):
         raise KVQError("kv_append_rope failed: KVQ_EINVAL (k and v, q, or all three)")
-    n_rows, dt = first.shape[0], _dtype(first.dtype, "kv_append_rope")
-    for t, what in ((k, "k"), (v, "v"), (q, "q")):
-        if t is not None and (t.dtype != first.dtype or t.shape[0] != n_rows or t.device != first.device):
-            raise KVQError(f"kv_append_rope: {what} differs from the other rows in type, number or device")
-    ks, vs = (0, 0) if k is None else (_rows(k, d.n_kv_heads, "k"), _rows(v, d.n_kv_heads, "v"))
-    qs = 0 if q is None else _rows(q, d.n_q_heads, "q")
-    n_seq, max_pages = page_table.shape
-    if row_start.numel() != n_seq + 1 or pos0.numel() != n_seq:
-        raise KVQError("kv_append_rope: row_start has n_seq + 1 entries and pos0 n_seq")
-    for t, what in ((row_start, "row_start"), (pos0, "pos0"), (page_table, "page_table")):
-        if t.dtype != torch.int32 or not t.is_contiguous():
-            raise KVQError(f"kv_append_rope: {what} is not a contiguous int32 tensor")
-    n_pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
-    if cos_sin is not None and (cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous()):
-        raise KVQError("kv_append_rope: cos_sin is not a contiguous float32 tensor")
-    if q is None:
+    n_rows, el = first.shape[0], first.dtype
+    dt = _dtype(el, "kv_append_rope")
+    kp = vp = qp = op = cp_ = None
+    ks = vs = qs = n_pos = rot = odt = 0
+    if k is not None:
+        ks, vs, kp, vp = _rows(k, d.n_kv_heads, "k"), _rows(v, d.n_kv_heads, "v"), k.data_ptr(), v.data_ptr()
+        if v.dtype is not el or v.shape[0] != n_rows:
+            raise KVQError("kv_append_rope: v differs from k in type or rows")
+    if q is not None:
+        qs, qp = _rows(q, d.n_q_heads, "q"), q.data_ptr()
+        if q.dtype is not el or q.shape[0] != n_rows:
+            raise KVQError("kv_append_rope: q differs from k in type or rows")
+        if q_out is None:
+            if q_out_dtype is None:
+                q_out_dtype = el if pool.fmt == FP8B else torch.float32
+            q_out = torch.empty((n_rows, d.n_q_heads, HEAD_DIM), dtype=q_out_dtype, device=q.device)
+        elif q_out.shape != q.shape or not q_out.is_contiguous():
+            raise KVQError("kv_append_rope: q_out is contiguous and shaped as q")
+        odt, op = _dtype(q_out.dtype, "kv_append_rope"), q_out.data_ptr()
+    else:
         q_out = None
-    elif q_out is None:
-        if q_out_dtype is None:
-            q_out_dtype = q.dtype if pool.fmt == FP8B else torch.float32
-        q_out = torch.empty((n_rows, d.n_q_heads, HEAD_DIM), dtype=q_out_dtype, device=q.device)
-    elif tuple(q_out.shape) != tuple(q.shape) or not q_out.is_contiguous():
-        raise KVQError("kv_append_rope: q_out is contiguous and shaped as q")
+    n_seq, max_pages = page_table.shape
+    if row_start.shape[0] != n_seq + 1 or pos0.shape[0] != n_seq:
+        raise KVQError("kv_append_rope: row_start has n_seq + 1 entries and pos0 n_seq")
+    rs, p0, pt = _index(row_start, "row_start"), _index(pos0, "pos0"), _index(page_table, "page_table")
+    if cos_sin is not None:
+        n_pos, rot = cos_sin.shape
+        if cos_sin.dtype is not torch.float32 or not cos_sin.is_contiguous():
+            raise KVQError("kv_append_rope: cos_sin is not a contiguous float32 tensor")
+        cp_ = cos_sin.data_ptr()
+    _on_current_device("kv_append_rope", first, v, q, q_out, row_start, pos0, page_table, cos_sin, status)
     cp = pool.c_pool()
-    _check(lib().kv_append_rope(ctypes.byref(cp), layer, _ptr(cos_sin), n_pos, rot, 1 if interleaved else 0, _ptr(q),
-                                _ptr(k), _ptr(v), dt, qs, ks, vs, n_rows, _ptr(row_start), _ptr(pos0),
-                                _ptr(page_table), max_pages, n_seq, _ptr(q_out),
-                                0 if q_out is None else _dtype(q_out.dtype, "kv_append_rope"), _ptr(status),
-                                _stream(stream)), "kv_append_rope")
+    _check(lib().kv_append_rope(ctypes.byref(cp), layer, cp_, n_pos, rot, 1 if interleaved else 0, qp, kp, vp, dt, qs, ks, vs,
+                                n_rows, rs, p0, pt, max_pages, n_seq, op, odt, _ptr(status), _stream(stream)),
+           "kv_append_rope")
     return q_out
 
 
@@ -408,18 +433,26 @@ def paged_prefill_attn_fp8b(pool: KVPool, layer: int, q, page_table, plan_dev, i
     them already: q [n_rows, n_q_heads, 256] (fp32, bf16 or fp16; rows may be
     strided), rotated as the keys are; plan_dev a device copy of prefill_plan's
     array; workspace None when info.workspace_bytes is 0."""
+    what = "paged_prefill_attn_fp8b"
+    qs = _rows(q, pool.desc.n_q_heads, "q")
     if q.shape[0] < info.n_rows:
-        raise KVQError("paged_prefill_attn_fp8b: q has fewer rows than the plan")
-    for t in (out_bf16, out_f32):
-        if t is not None and (tuple(t.shape[1:]) != tuple(q.shape[1:]) or t.shape[0] < info.n_rows or
-                              not t.is_contiguous()):
-            raise KVQError("paged_prefill_attn_fp8b: an output is contiguous and shaped as q")
+        raise KVQError(f"{what}: q has fewer rows than the plan")
+    import torch
+    for t, el in ((out_bf16, torch.bfloat16), (out_f32, torch.float32)):
+        if t is not None and (t.shape[1:] != q.shape[1:] or t.shape[0] < info.n_rows or not t.is_contiguous() or
+                              t.dtype is not el):
+            raise KVQError(f"{what}: an output is contiguous, of its type and shaped as q")
+    if page_table.shape[0] < info.n_seq:
+        raise KVQError(f"{what}: page_table has fewer sequences than the plan")
+    pt, pl = _index(page_table, "page_table"), _index(plan_dev, "plan_dev")
+    if plan_dev.shape[0] < info.plan_len:
+        raise KVQError(f"{what}: plan_dev is shorter than the plan")
+    _on_current_device(what, q, page_table, plan_dev, workspace, out_bf16, out_f32, status)
     cp = pool.c_pool()
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().paged_prefill_attn_fp8b(ctypes.byref(cp), layer, _ptr(q), _dtype(q.dtype, "paged_prefill_attn_fp8b"),
-                                         _rows(q, pool.desc.n_q_heads, "q"), _ptr(page_table), page_table.shape[1],
-                                         _ptr(plan_dev), ctypes.byref(info), _ptr(workspace), ws_bytes, _ptr(out_bf16),
-                                         _ptr(out_f32), _ptr(status), _stream(stream)), "paged_prefill_attn_fp8b")
+    _check(lib().paged_prefill_attn_fp8b(ctypes.byref(cp), layer, q.data_ptr(), _dtype(q.dtype, what), qs, pt,
+                                         page_table.shape[1], pl, ctypes.byref(info), _ptr(workspace), ws_bytes,
+                                         _ptr(out_bf16), _ptr(out_f32), _ptr(status), _stream(stream)), what)
 
 
 def prefill_split(desc: PoolDesc, pos0: int, n_tok: int, n_sms: int = 0):
