@@ -207,9 +207,13 @@ int kv_append_q_rotate(const kvq_pool *pool, int layer, const float *k, const fl
  * filled with the plan (copy it to the device as is).  info receives the
  * sizes, including the workspace bytes the decode/combine pair needs.
  * KVQ_ESIZE if plan_capacity is too small (info->plan_len then holds the
- * needed length). */
+ * needed length).
+ * For an fp8b descriptor the ranges are laid end to end and cut into n_ctas equal
+ * shares, so a CTA may take several units and n_units may pass n_ctas by up to
+ * n_seq * n_kv_heads; such a plan fits only the fp8b entry points and
+ * attn_combine. */
 typedef struct {
-    int32_t n_units;        /* work units = CTAs of the decode launch */
+    int32_t n_units;        /* work units = CTAs of the decode launch (fp8b: CTAs take several) */
     int32_t n_seq;
     int32_t n_kv_heads;
     int32_t group;          /* query heads per KV head */

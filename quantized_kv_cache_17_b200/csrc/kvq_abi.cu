@@ -73,6 +73,90 @@ int check_pool(const kvq_pool *pool, int layer, PoolGeom *geo) {
 // merge moves as many bytes as four steps read).
 constexpr int64_t PFB_TILE_COST = 8, PFB_MIN_PART = 4;
 
+// Decode plan of fp8b: what a unit costs beyond its steps of 64 tokens (query,
+// merge of the warps, result: about 1.5 us, 0.75 us a step) and the shortest unit
+// worth cutting off.
+constexpr int64_t BD_UNIT_COST = 2, BD_MIN_PART = 2;
+
+// The (sequence, KV head) ranges one after another, cut where a CTA has its share,
+// so that a CTA takes consecutive units and all CTAs about the same; the units
+// start table is followed by the CTAs' (n_ctas + 1 entries, header entry 6 holds
+// n_ctas).  Ranges that are longer or shorter than a share need no CTA of their
+// own: four sequences of 8,192 to 262,144 tokens differ by 1 % between CTAs, where
+// whole CTAs per range leave 13 %.
+int block_decode_plan(int n_seq, int n_kv, int G, const int32_t *seq_len, int n_ctas, int32_t *plan, int plan_capacity,
+                      kvq_plan_info *info) {
+    const int64_t groups = (int64_t)n_seq * n_kv;
+    auto steps_of = [&](int b) { return ((int64_t)seq_len[b] + STEP_TOKENS - 1) / STEP_TOKENS; };
+    int64_t total = 0, longest = 0;
+    for (int b = 0; b < n_seq; ++b) total += (steps_of(b) + BD_UNIT_COST) * n_kv;
+    if (groups > (1 << 24)) return KVQ_EUNSUPPORTED;
+    struct Count {
+        int64_t units = 0, ctas = 0;
+    };
+    auto walk = [&](int64_t share, int32_t *U, int32_t *start, int32_t *cta) {
+        Count c;
+        int64_t used = 0;
+        if (cta) cta[0] = 0;
+        auto close = [&]() {
+            ++c.ctas;
+            used = 0;
+            if (cta) cta[c.ctas] = (int32_t)c.units;
+        };
+        longest = 0;
+        for (int b = 0; b < n_seq; ++b)
+            for (int g = 0; g < n_kv; ++g) {
+                if (start) start[(int64_t)b * n_kv + g] = (int32_t)c.units;
+                const int64_t steps = steps_of(b);
+                for (int64_t s0 = 0; s0 < steps;) {
+                    const int64_t room = share - used - BD_UNIT_COST, rest = steps - s0;
+                    if (room < BD_MIN_PART && rest > room && used > 0) {
+                        close();
+                        continue;
+                    }
+                    const int64_t n = rest < room + BD_MIN_PART ? rest : std::max(room, BD_MIN_PART);
+                    if (U) {
+                        int32_t *u = U + 4 * c.units;
+                        u[0] = b;
+                        u[1] = g;
+                        u[2] = (int32_t)(s0 * STEP_TOKENS);
+                        u[3] = (int32_t)std::min<int64_t>((s0 + n) * STEP_TOKENS, seq_len[b]);
+                    }
+                    ++c.units;
+                    s0 += n;
+                    used += n + BD_UNIT_COST;
+                    longest = std::max(longest, n);
+                    if (used >= share) close();
+                }
+            }
+        if (used > 0) close();
+        if (start) start[groups] = (int32_t)c.units;
+        return c;
+    };
+    int64_t lo = std::max<int64_t>(BD_MIN_PART + BD_UNIT_COST, (total + n_ctas - 1) / n_ctas), hi = std::max(lo, total);
+    while (lo < hi) {                      // a share of the whole total needs one CTA
+        const int64_t mid = lo + (hi - lo) / (hi > 2 * lo ? 16 : 2);
+        if (walk(mid, nullptr, nullptr, nullptr).ctas <= n_ctas) hi = mid;
+        else lo = mid + 1;
+    }
+    const Count c = walk(lo, nullptr, nullptr, nullptr);
+    if (c.units > (1 << 24)) return KVQ_EUNSUPPORTED;
+    const int64_t len = (int64_t)plan_len_for((int)c.units, n_seq, n_kv) + c.ctas + 1;
+    info->n_units = (int32_t)c.units;
+    info->n_seq = n_seq;
+    info->n_kv_heads = n_kv;
+    info->group = G;
+    info->plan_len = (int32_t)len;
+    info->chunk_tokens = (int32_t)(longest * STEP_TOKENS);
+    info->workspace_bytes = ws_bytes_for((int)c.units, G, (int)groups);
+    if (!plan || plan_capacity < len) return KVQ_ESIZE;
+    const int32_t head[PLAN_HEADER] = {PLAN_MAGIC, (int32_t)c.units, n_seq, n_kv, G, info->chunk_tokens, (int32_t)c.ctas, 0};
+    std::copy(head, head + PLAN_HEADER, plan);
+    int32_t *U = plan + PLAN_HEADER, *start = U + 4 * c.units;
+    walk(lo, U, start, start + groups + 1);
+    return KVQ_OK;
+}
+
 int cuda_rc(cudaError_t e) { return e == cudaSuccess ? KVQ_OK : KVQ_ECUDA; }
 
 }  // namespace
@@ -111,10 +195,13 @@ int decode_common(int fmt, bool tc, const kvq_pool *pool, int layer, const float
     const int rc = check_decode_args(fmt, pool, layer, q, page_table, max_pages, plan, info, workspace_bytes,
                                      out_bf16, out_f32, &geo);
     if (rc) return rc;
-    if (fmt == KVQ_FP8B)
+    if (fmt == KVQ_FP8B) {
+        const int64_t n_ctas = (int64_t)info->plan_len - plan_len_for(info->n_units, info->n_seq, info->n_kv_heads) - 1;
+        if (n_ctas < 1 || n_ctas > info->n_units) return KVQ_EINVAL;      // another format's plan
         return cuda_rc(launch_block_decode(static_cast<const uint8_t *>(pool->base), geo, layer, q, page_table, max_pages,
-                                           plan, *info, workspace, status, out_bf16, out_f32,
+                                           plan, *info, (int)n_ctas, workspace, status, out_bf16, out_f32,
                                            static_cast<cudaStream_t>(stream)));
+    }
     const int inverse = host_rotated_v(fmt) ? 1 : 0;
     return cuda_rc(launch_decode(fmt, tc, static_cast<const uint8_t *>(pool->base), geo, layer, q, page_table,
                                  max_pages, plan, *info, workspace, status, inverse, out_bf16, out_f32,
@@ -212,6 +299,7 @@ int kvq_decode_plan(const kvq_pool_desc *desc, int n_seq, const int32_t *seq_len
             return KVQ_ECUDA;
         n_ctas = sms;   // one decode CTA per SM
     }
+    if (desc->fmt == KVQ_FP8B) return block_decode_plan(n_seq, n_kv, G, seq_len, n_ctas, plan, plan_capacity, info);
     auto units_for = [&](int64_t c) {
         int64_t n = 0;
         for (int b = 0; b < n_seq; ++b) n += n_kv * ((steps[b] + c - 1) / c);

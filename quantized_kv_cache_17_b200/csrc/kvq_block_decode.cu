@@ -1,11 +1,11 @@
 // paged_decode_attn_fp8b: single-token attention over the fp8b pool (E4M3 codes,
 // one power-of-two scale for K and one for V per 64 tokens of a KV head).
 //
-// Per unit of the split plan, one CTA streams the unit's tiles (64 tokens, 32 KB
-// of codes, contiguous) through a ring of bulk copies.  A tile goes to four of
-// the eight compute warps, 16 of its tokens each; even tiles to warps 0-3, odd
-// ones to warps 4-7.  A warp does scores, softmax and values of its 16 tokens
-// with nothing exchanged between warps until the unit ends:
+// A CTA takes consecutive units of the plan and streams their tiles (64 tokens,
+// 32 KB of codes, contiguous) through a ring of bulk copies that runs on from unit
+// to unit.  A tile goes to four of the twelve compute warps, 16 of its tokens
+// each; the three sets of four take turns.  A warp does scores, softmax and
+// values of its 16 tokens with nothing exchanged between warps until the unit ends:
 //   S[8 heads][16 tokens] = Q K^T, m16n8k16 in fp16.  Codes are exact in fp16.
 //     The query rows are fp16 high parts (rows 0-7) and low parts (rows 8-15) of
 //     q 2^kq, so the product keeps 22 bits of q at no extra instruction.
@@ -24,25 +24,30 @@
 namespace kvq {
 namespace {
 
+constexpr int BD_SETS = 3, BD_WARPS = 4 * BD_SETS;    // compute warps, four to a tile
+constexpr int BD_THREADS = (BD_WARPS + 4) * 32;       // and a warpgroup whose first warp copies
+constexpr int BD_REGS = 128, BD_REGS_COMPUTE = 152, BD_REGS_REST = 56;   // a thread's registers at launch and after setmaxnreg
+static_assert(BD_SETS * BD_REGS_COMPUTE + BD_REGS_REST <= 4 * BD_REGS, "the compute warps take what the others give back");
+// A multiple of the sets, and a tile's set goes by its place in the CTA's stream, so that a stage always belongs to the same
+// four warps: a set that skipped uses of a stage could take an older phase of its barrier, of the same parity, for the one it
+// waits for.
 constexpr int BD_STAGES = 6;
-constexpr int BD_WARPS = 8;                       // compute warps
-constexpr int BD_THREADS = (BD_WARPS + 1) * 32;   // and the copy warp
+static_assert(BD_STAGES % BD_SETS == 0, "stages per set");
 constexpr uint64_t BD_WAIT_NS = 2000000000ull;
 constexpr int BD_OSTRIDE = 260;                   // floats of a head's row in the merge: heads 2t, 2t+1 of a store fall on their own banks
 constexpr int BD_RING = BD_STAGES * BT_BYTES;
-// after the ring: the query (8 x 256 fp32), scales, barriers, softmax state
-struct BdTail {
-    float q[8][D];
+struct BdTail {                                   // after the ring
+    union {
+        uint4 q[16][32];                          // query fragments [k-step][lane], until a unit's last tile
+        float o[4][8][BD_OSTRIDE];                // merge of the warps, after it
+    };
     float scale[BD_STAGES][4];                    // the 16 bytes that hold the tile's scales
-    float m[BD_WARPS][8], l[BD_WARPS][8];
-    float e[BD_WARPS];
-    float w[BD_WARPS][8];
-    float L[8];
+    float m[BD_WARPS][8], l[BD_WARPS][8], M[8], L[8], qscale[8];
     uint64_t full[BD_STAGES], empty[BD_STAGES];
     int slot_ok[BD_STAGES];
 };
 constexpr int BD_SMEM = BD_RING + (int)sizeof(BdTail) + 1024;   // 1,024: the ring starts on an atom's boundary
-static_assert(BD_WARPS * 8 * BD_OSTRIDE * 4 <= BD_RING, "merge buffers fit in the ring");
+static_assert(BD_SMEM <= 232448, "227 KB a CTA");
 
 struct BdArgs {
     const uint8_t *pool;
@@ -52,7 +57,7 @@ struct BdArgs {
     const int32_t *page_table;
     int max_pages;
     const int32_t *plan;
-    int n_units, n_seq, n_q_heads, G;
+    int n_units, n_ctas, n_seq, n_q_heads, G;
     float *ws;
     int32_t *status;
     uint16_t *out_bf16;       // null: every unit leaves a partial
@@ -67,155 +72,205 @@ __device__ __forceinline__ void write_out(const BdArgs &A, int64_t row, int dim,
     if (A.out_f32) A.out_f32[row * D + dim] = x;
 }
 
+struct BdUnit {
+    int seq, kvh, t0, t1;
+};
+// Unit i of the plan; false when it does not fit the call.
+__device__ __forceinline__ bool load_unit(const BdArgs &A, int i, BdUnit &u) {
+    const int32_t *p = A.plan + PLAN_HEADER + 4 * (int64_t)i;
+    u = BdUnit{__ldg(p), __ldg(p + 1), __ldg(p + 2), __ldg(p + 3)};
+    return u.seq >= 0 && u.seq < A.n_seq && u.kvh >= 0 && u.kvh < A.geo.n_kv_heads && u.t0 >= 0 && u.t0 < u.t1 &&
+           u.t0 % BT == 0 && u.t1 <= A.max_pages * PAGE;
+}
+
 __global__ void __launch_bounds__(BD_THREADS, 1) block_decode_kernel(BdArgs A) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     BdTail &T = *reinterpret_cast<BdTail *>(ring + BD_RING);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int G = A.G, unit = blockIdx.x;
-    grid_dependency_wait();
-    const int32_t *u = A.plan + PLAN_HEADER + 4 * unit;
-    const int seq = u[0], kvh = u[1], t0 = u[2], t1 = u[3];
-    float *wsu = A.ws + (int64_t)unit * ws_unit_floats(G);
-    if (A.plan[0] != PLAN_MAGIC || A.plan[1] != A.n_units || A.plan[2] != A.n_seq || A.plan[3] != A.geo.n_kv_heads ||
-        seq < 0 || seq >= A.n_seq || kvh < 0 || kvh >= A.geo.n_kv_heads || t0 < 0 || t0 >= t1 || t0 % BT != 0 ||
-        t1 > A.max_pages * PAGE) {
-        if (tid == 0) status_or(A.status, KVQ_STATUS_BAD_PLAN);
-        for (int i = tid; i < G * D; i += BD_THREADS) wsu[i] = 0.0f;
-        if (tid < 8) wsu[G * D + tid] = -INFINITY, wsu[G * D + 8 + tid] = 0.0f;
-        return;
-    }
-    const int n_tiles = (t1 - t0 + BT - 1) / BT;
+    const int G = A.G;
     if (tid < BD_STAGES) {
         mbar_init(&T.full[tid], 1);
         mbar_init(&T.empty[tid], 4);
     }
     fence_mbar_init();
     __syncthreads();
+    // the merge kernel may take its place on the SMs now; it waits for this grid's end before it reads
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_dependency_wait();
+    const bool good = __ldg(A.plan) == PLAN_MAGIC && __ldg(A.plan + 1) == A.n_units && __ldg(A.plan + 2) == A.n_seq &&
+                      __ldg(A.plan + 3) == A.geo.n_kv_heads && __ldg(A.plan + 6) == A.n_ctas;
+    if (!good && tid == 0) status_or(A.status, KVQ_STATUS_BAD_PLAN);
+    const int32_t *start = A.plan + PLAN_HEADER + 4 * (int64_t)A.n_units;
+    const int32_t *cta = start + A.n_seq * A.geo.n_kv_heads + 1;
+    const int i0 = good ? max(0, __ldg(cta + blockIdx.x)) : 0, i1 = good ? min(A.n_units, __ldg(cta + blockIdx.x + 1)) : 0;
 
-    if (warp == BD_WARPS) {                        // ---- copy warp ----
+    if (warp >= BD_WARPS) {                        // ---- copies ----
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(BD_REGS_REST));
+        if (warp > BD_WARPS) return;
         const uint64_t policy = policy_evict_first();
-        const int32_t *row = A.page_table + (int64_t)seq * A.max_pages;
-        const uint8_t *base = A.pool + A.layer * A.geo.layer_stride + (int64_t)kvh * A.geo.page_bytes;
-        const int page0 = t0 >> 8, page_end = (t1 + PAGE - 1) >> 8;
-        int held = -1, held_from = page0 - 32, i = 0;
-        for (; i < n_tiles; ++i) {
-            const int tile = (t0 >> 6) + i, page = tile >> 2, s = i % BD_STAGES, use = i / BD_STAGES;
-            if (page >= held_from + 32) {          // 32 page-table entries at a time
-                held_from = page;
-                held = page + lane < page_end ? __ldg(row + page + lane) : -1;
-            }
-            const int slot = __shfl_sync(0xffffffffu, held, page - held_from);
-            if (use > 0 && !mbar_wait_bounded(&T.empty[s], (use - 1) & 1, BD_WAIT_NS)) {
-                if (lane == 0) status_or(A.status, KVQ_STATUS_TIMEOUT);
-                break;
-            }
-            __syncwarp();
-            if (lane == 0) {
-                const bool ok = slot >= 0 && slot < A.geo.n_pages;
-                T.slot_ok[s] = ok;
-                if (ok) {
-                    const uint8_t *blk = base + (int64_t)slot * A.geo.slot_stride;
-                    mbar_arrive_expect_tx(&T.full[s], BT_BYTES + 16);
-                    bulk_g2s(T.scale[s], blk + B_SCALES_OFF + ((tile & 3) >> 1) * 16, 16, &T.full[s], policy);
-                    bulk_g2s(ring + s * BT_BYTES, blk + (tile & 3) * BT_BYTES, BT_BYTES, &T.full[s], policy);
-                } else {
-                    status_or(A.status, KVQ_STATUS_BAD_SLOT);
-                    mbar_arrive(&T.full[s]);
+        int it = 0;
+        bool ok = true;
+        for (int i = i0; i < i1 && ok; ++i) {
+            BdUnit u;
+            if (!load_unit(A, i, u)) continue;
+            const int n_tiles = (u.t1 - u.t0 + BT - 1) / BT;
+            const int32_t *row = A.page_table + (int64_t)u.seq * A.max_pages;
+            const uint8_t *base = A.pool + A.layer * A.geo.layer_stride + (int64_t)u.kvh * A.geo.page_bytes;
+            const int page_end = (u.t1 + PAGE - 1) >> 8;
+            int held = -1, held_from = (u.t0 >> 8) - 32;
+            for (int j = 0; j < n_tiles; ++j, ++it) {
+                const int tile = (u.t0 >> 6) + j, page = tile >> 2, s = it % BD_STAGES, use = it / BD_STAGES;
+                if (page >= held_from + 32) {      // 32 page-table entries at a time
+                    held_from = page;
+                    held = page + lane < page_end ? __ldg(row + page + lane) : -1;
                 }
+                const int slot = __shfl_sync(0xffffffffu, held, page - held_from);
+                if (use > 0 && !__all_sync(0xffffffffu, mbar_wait_bounded(&T.empty[s], (use - 1) & 1, BD_WAIT_NS))) {
+                    if (lane == 0) status_or(A.status, KVQ_STATUS_TIMEOUT);
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) {
+                    const bool there = slot >= 0 && slot < A.geo.n_pages;
+                    T.slot_ok[s] = there;
+                    if (there) {
+                        const uint8_t *blk = base + (int64_t)slot * A.geo.slot_stride;
+                        mbar_arrive_expect_tx(&T.full[s], BT_BYTES + 16);
+                        bulk_g2s(T.scale[s], blk + B_SCALES_OFF + ((tile & 3) >> 1) * 16, 16, &T.full[s], policy);
+                        bulk_g2s(ring + s * BT_BYTES, blk + (tile & 3) * BT_BYTES, BT_BYTES, &T.full[s], policy);
+                    } else {
+                        status_or(A.status, KVQ_STATUS_BAD_SLOT);
+                        mbar_arrive(&T.full[s]);
+                    }
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
         // no copy is left in flight
-        for (int o = max(0, i - BD_STAGES); o < i; ++o) mbar_wait_bounded(&T.full[o % BD_STAGES], (o / BD_STAGES) & 1, BD_WAIT_NS);
-    } else {
-        // ---- query: head `warp` to shared memory, then fragments ----
-        {
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-            if (warp < G) {
-                const float4 *p = reinterpret_cast<const float4 *>(A.q + ((int64_t)seq * A.n_q_heads + kvh * G + warp) * D);
-                a = __ldg(p + lane);
-                b = __ldg(p + 32 + lane);
-            }
-            reinterpret_cast<float4 *>(T.q[warp])[lane] = a;
-            reinterpret_cast<float4 *>(T.q[warp])[lane + 32] = b;
+        for (int o = max(0, it - BD_STAGES); o < it; ++o) mbar_wait_bounded(&T.full[o % BD_STAGES], (o / BD_STAGES) & 1, BD_WAIT_NS);
+        return;
+    }
+
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(BD_REGS_COMPUTE));
+    auto sync = [] { asm volatile("bar.sync 1, %0;" ::"n"(BD_WARPS * 32) : "memory"); };
+    // head `warp` of a unit's query
+    auto load_query = [&](const BdUnit &u, float4 &a, float4 &b) {
+        a = b = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (warp < G) {
+            const float4 *p = reinterpret_cast<const float4 *>(A.q + ((int64_t)u.seq * A.n_q_heads + u.kvh * G + warp) * D);
+            a = __ldg(p + lane);
+            b = __ldg(p + 32 + lane);
         }
-        asm volatile("bar.sync 1, %0;" ::"n"(BD_WARPS * 32) : "memory");
-        // k-step (h, i, x): lane t holds the dims 128 h + 16 (2 t + i) + 4 x + 0 .. 3
-        uint32_t qf[16][4];
-        float qscale;
-        {
+    };
+    const int set = warp >> 2, w4 = warp & 3;
+    int it = 0;                                    // tiles of the units before
+    bool alive = true;
+    BdUnit u;
+    bool fits = i0 < i1 && load_unit(A, i0, u);
+    float4 qa, qb;
+    if (fits) load_query(u, qa, qb);
+    for (int i = i0; i < i1; ++i) {
+        float *wsu = A.ws + (int64_t)i * ws_unit_floats(G);
+        BdUnit next;
+        const bool next_fits = i + 1 < i1 && load_unit(A, i + 1, next);
+        if (!fits) {                               // an empty partial, which the merge ignores
+            if (tid == 0) status_or(A.status, KVQ_STATUS_BAD_PLAN);
+            for (int x = tid; x < G * D; x += BD_WARPS * 32) wsu[x] = 0.0f;
+            if (tid < 8) wsu[G * D + tid] = -INFINITY, wsu[G * D + 8 + tid] = 0.0f;
+            u = next;
+            fits = next_fits;
+            if (fits) load_query(u, qa, qb);
+            continue;
+        }
+        const int seq = u.seq, kvh = u.kvh, t0 = u.t0, t1 = u.t1, n_tiles = (t1 - t0 + BT - 1) / BT;
+        // ---- query fragments, head `warp`.  k-step s = (h, i, x): lane (g, t) takes the dims 128 h + 16 (2 t + i) + 4 x + 0 .. 3
+        // of head g, which are four floats of one lane here ----
+        if (warp < 8) {
+            const float4 v[2] = {qa, qb};
             float mx = 0.0f;
-            for (int i = 0; i < 64; ++i) mx = fmaxf(mx, fabsf(T.q[g][(i * 4 + t) & 255]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) mx = fmaxf(fmaxf(mx, fmaxf(fabsf(v[h].x), fabsf(v[h].y))), fmaxf(fabsf(v[h].z), fabsf(v[h].w)));
+            mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));       // not negative: the bits order as the values
             // 2^kq puts the head's largest |q| into [2^12, 2^13)
             const int kq = mx > 0.0f ? max(-114, min(114, 12 - ((int)(__float_as_uint(mx) >> 23) - 127))) : 0;
             const float up = pow2i(kq);
-            qscale = pow2i(-kq) * (1.4426950408889634f / 16.0f);
+            if (lane == 0) T.qscale[warp] = pow2i(-kq) * (1.4426950408889634f / 16.0f);
 #pragma unroll
-            for (int s = 0; s < 16; ++s) {
-                const float4 v = *reinterpret_cast<const float4 *>(&T.q[g][128 * (s >> 3) + 16 * (2 * t + ((s >> 2) & 1)) + 4 * (s & 3)]);
-                const float f[4] = {v.x * up, v.y * up, v.z * up, v.w * up};
-                __half2 hi[2], lo[2];
+            for (int h = 0; h < 2; ++h) {
+                const float f[4] = {v[h].x * up, v[h].y * up, v[h].z * up, v[h].w * up};
+                uint32_t hi[2], lo[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    hi[j] = __floats2half2_rn(f[2 * j], f[2 * j + 1]);
-                    const float2 r = __half22float2(hi[j]);
-                    lo[j] = __floats2half2_rn(f[2 * j] - r.x, f[2 * j + 1] - r.y);
+                    const __half2 a = __floats2half2_rn(f[2 * j], f[2 * j + 1]);
+                    const float2 r = __half22float2(a);
+                    hi[j] = h2_as_u32(a);
+                    lo[j] = h2_as_u32(__floats2half2_rn(f[2 * j] - r.x, f[2 * j + 1] - r.y));
                 }
-                qf[s][0] = h2_as_u32(hi[0]);
-                qf[s][1] = h2_as_u32(lo[0]);
-                qf[s][2] = h2_as_u32(hi[1]);
-                qf[s][3] = h2_as_u32(lo[1]);
+                T.q[8 * h + 4 * ((lane >> 2) & 1) + (lane & 3)][4 * warp + (lane >> 3)] = make_uint4(hi[0], lo[0], hi[1], lo[1]);
             }
         }
+        sync();
+        const float qscale = T.qscale[g];
         float o[16][4];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+        for (int x = 0; x < 16; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.0f;
         float m = -INFINITY, l = 0.0f;             // of head g; l over this lane's tokens
         int E = -10000;                            // o is in units of 2^(E - 7)
-        const int set = warp >> 2, w4 = warp & 3;
-        for (int i = set; i < n_tiles; i += 2) {
-            const int s = i % BD_STAGES;
-            if (!mbar_wait_bounded(&T.full[s], (i / BD_STAGES) & 1, BD_WAIT_NS)) {
+        for (int j = (set + BD_SETS - it % BD_SETS) % BD_SETS; j < n_tiles && alive; j += BD_SETS) {
+            const int s = (it + j) % BD_STAGES;
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&T.full[s], ((it + j) / BD_STAGES) & 1, BD_WAIT_NS))) {
                 if (lane == 0) status_or(A.status, KVQ_STATUS_TIMEOUT);
+                alive = false;                     // this warp computes no more, but keeps the barriers
                 break;
             }
-            const int tok = t0 + i * BT + 16 * w4 + 4 * t;      // this lane's four tokens
+            const int tok = t0 + j * BT + 16 * w4 + 4 * t;      // this lane's four tokens
             const int valid = min(4, max(0, t1 - tok));
-            if (T.slot_ok[s] && t0 + i * BT + 16 * w4 < t1) {
+            if (T.slot_ok[s] && t0 + j * BT + 16 * w4 < t1) {
                 const uint8_t *kt = ring + s * BT_BYTES, *vt = kt + BT_K_BYTES;
-                const int half = ((t0 >> 6) + i) & 1;
+                const int half = ((t0 >> 6) + j) & 1;
                 const float dk = T.scale[s][2 * half], dv = T.scale[s][2 * half + 1];
                 float sc[2][2][4];                 // [score tile][accumulator of the dim half]
+                const uint8_t *kr[2];
+                int row7[2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const int row = 16 * w4 + 4 * (g >> 1) + 2 * j + (g & 1);
-                    const uint8_t *kr = kt + (row >> 3) * 1024 + (row & 7) * 128;
+                for (int y = 0; y < 2; ++y) {
+                    const int row = 16 * w4 + 4 * (g >> 1) + 2 * y + (g & 1);
+                    kr[y] = kt + (row >> 3) * 1024 + (row & 7) * 128;
+                    row7[y] = row & 7;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float (&c)[4] = sc[j][h];
-                        c[0] = c[1] = c[2] = c[3] = 0.0f;
+                    for (int h = 0; h < 2; ++h) sc[y][h][0] = sc[y][h][1] = sc[y][h][2] = sc[y][h][3] = 0.0f;
+                }
 #pragma unroll
-                        for (int ii = 0; ii < 2; ++ii) {
-                            const uint4 w = lds128(kr + h * 8192 + (((2 * t + ii) ^ (row & 7)) << 4));
-                            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                for (int ii = 0; ii < 2; ++ii) {
+                    uint32_t kw[2][2][4];
 #pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                mma16816(c, qf[8 * h + 4 * ii + x], e4m3x2_to_h2(ws[x] & 0xFFFFu), e4m3x2_to_h2(ws[x] >> 16));
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint4 w = lds128(kr[y] + h * 8192 + (((2 * t + ii) ^ row7[y]) << 4));
+                            kw[y][h][0] = w.x; kw[y][h][1] = w.y; kw[y][h][2] = w.z; kw[y][h][3] = w.w;
                         }
-                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint4 w = lds128(&T.q[8 * h + 4 * ii + x][lane]);
+                            const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+                                mma16816(sc[y][h], q, e4m3x2_to_h2(kw[y][h][x] & 0xFFFFu), e4m3x2_to_h2(kw[y][h][x] >> 16));
+                        }
                 }
                 // scores of head g, tokens 4t .. 4t + 3: high and low rows, both dim halves
                 const float f = dk * qscale;
                 float p[4];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                for (int y = 0; y < 2; ++y)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const float v = (sc[j][0][x] + sc[j][1][x] + (sc[j][0][x + 2] + sc[j][1][x + 2])) * f;
-                        p[2 * j + x] = 2 * j + x < valid ? v : -INFINITY;
+                        const float v = (sc[y][0][x] + sc[y][1][x] + (sc[y][0][x + 2] + sc[y][1][x + 2])) * f;
+                        p[2 * y + x] = 2 * y + x < valid ? v : -INFINITY;
                     }
                 float mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
@@ -240,13 +295,13 @@ __global__ void __launch_bounds__(BD_THREADS, 1) block_decode_kernel(BdArgs A) {
                 const float wv = ev < -5000 ? 0.0f : pow2i(ev - E + 7);
                 uint32_t whi[2], wlo[2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float p0 = ex2(p[2 * j] - mref), p1 = ex2(p[2 * j + 1] - mref);
+                for (int y = 0; y < 2; ++y) {
+                    const float p0 = ex2(p[2 * y] - mref), p1 = ex2(p[2 * y + 1] - mref);
                     l += p0 + p1;
                     const __half2 h = __floats2half2_rn(p0 * wv, p1 * wv);
                     const float2 r = __half22float2(h);
-                    whi[j] = h2_as_u32(h);
-                    wlo[j] = h2_as_u32(__floats2half2_rn(p0 * wv - r.x, p1 * wv - r.y));
+                    whi[y] = h2_as_u32(h);
+                    wlo[y] = h2_as_u32(__floats2half2_rn(p0 * wv - r.x, p1 * wv - r.y));
                 }
                 const uint32_t keep = valid == 4 ? 0xFFFFFFFFu : (1u << (8 * valid)) - 1u;   // codes past the end may be NaN
 #pragma unroll
@@ -262,46 +317,62 @@ __global__ void __launch_bounds__(BD_THREADS, 1) block_decode_kernel(BdArgs A) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&T.empty[s]);
         }
+        it += n_tiles;
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
         if (t == 0) T.m[warp][g] = m, T.l[warp][g] = l;
-        // o in true units would be o 2^(E - 7): the exponent goes into the warp's weight
-        if (lane == 0) T.e[warp] = E > -5000 ? exp2f((float)(E - 7)) : 0.0f;
-        asm volatile("bar.sync 1, %0;" ::"n"(BD_WARPS * 32) : "memory");
-        // ---- merge of the eight warps ----
-        float *buf = reinterpret_cast<float *>(ring);
-        if (tid < 64) {
-            const int w = tid >> 3, h = tid & 7;
-            float M = -INFINITY;
-            for (int x = 0; x < BD_WARPS; ++x) M = fmaxf(M, T.m[x][h]);
-            T.w[w][h] = T.m[w][h] == -INFINITY ? 0.0f : exp2f(T.m[w][h] - M);
-        }
+        if (next_fits) load_query(next, qa, qb);
+        sync();
+        // ---- merge of the warps: each brings its o to the unit's reference (true units: 2^(E - 7)) ----
+        {
+            const float eo = E > -5000 ? exp2f((float)(E - 7)) : 0.0f;
+            float f[2];
 #pragma unroll
-        for (int x = 0; x < 16; ++x)
+            for (int x = 0; x < 2; ++x) {
+                float M = T.m[0][2 * t + x];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) buf[(warp * 8 + 2 * t + (c & 1)) * BD_OSTRIDE + 16 * x + g + 8 * (c >> 1)] = o[x][c];
-        asm volatile("bar.sync 1, %0;" ::"n"(BD_WARPS * 32) : "memory");
-        const int32_t *start = A.plan + PLAN_HEADER + 4 * A.n_units + seq * A.geo.n_kv_heads + kvh;
-        const bool whole = A.out_bf16 && start[0] == unit && start[1] == unit + 1;
-        for (int h = 0; h < G; ++h) {
-            float acc = 0.0f, L = 0.0f;
-#pragma unroll
-            for (int w = 0; w < BD_WARPS; ++w) {
-                acc = fmaf(buf[(w * 8 + h) * BD_OSTRIDE + tid], T.w[w][h] * T.e[w], acc);
-                L = fmaf(T.l[w][h], T.w[w][h], L);
+                for (int w = 1; w < BD_WARPS; ++w) M = fmaxf(M, T.m[w][2 * t + x]);
+                const float mine = T.m[warp][2 * t + x];
+                f[x] = mine == -INFINITY ? 0.0f : ex2(mine - M) * eo;
             }
-            if (whole) {
-                write_out(A, (int64_t)seq * A.n_q_heads + kvh * G + h, tid, L > 0.0f ? acc / L : 0.0f);
-            } else {
-                wsu[h * D + tid] = acc;
-                if (tid == 0) {
-                    float M = -INFINITY;
-                    for (int x = 0; x < BD_WARPS; ++x) M = fmaxf(M, T.m[x][h]);
-                    wsu[G * D + h] = M;
-                    wsu[G * D + 8 + h] = L;
+            if (tid < 8) {                         // head tid: the reference and the sum, for later
+                float M = T.m[0][tid], L = 0.0f;
+#pragma unroll
+                for (int w = 1; w < BD_WARPS; ++w) M = fmaxf(M, T.m[w][tid]);
+#pragma unroll
+                for (int w = 0; w < BD_WARPS; ++w) L = fmaf(T.l[w][tid], T.m[w][tid] == -INFINITY ? 0.0f : ex2(T.m[w][tid] - M), L);
+                T.M[tid] = M;
+                T.L[tid] = L;
+            }
+#pragma unroll
+            for (int turn = BD_SETS - 1; turn >= 0; --turn) {       // the sets add theirs one after another
+                if (set == turn)
+#pragma unroll
+                    for (int x = 0; x < 16; ++x)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            float &to = T.o[w4][2 * t + (c & 1)][16 * x + g + 8 * (c >> 1)];
+                            to = turn == BD_SETS - 1 ? o[x][c] * f[c & 1] : fmaf(o[x][c], f[c & 1], to);
+                        }
+                sync();
+            }
+        }
+        const int32_t *st = start + seq * A.geo.n_kv_heads + kvh;
+        const bool whole = A.out_bf16 && __ldg(st) == i && __ldg(st + 1) == i + 1;
+        if (tid < D)
+            for (int h = 0; h < G; ++h) {
+                const float acc = (T.o[0][h][tid] + T.o[1][h][tid]) + (T.o[2][h][tid] + T.o[3][h][tid]);
+                if (whole) {
+                    const float L = T.L[h];
+                    write_out(A, (int64_t)seq * A.n_q_heads + kvh * G + h, tid, L > 0.0f ? acc / L : 0.0f);
+                } else {
+                    wsu[h * D + tid] = acc;
                 }
             }
-        }
+        if (!whole && tid < G) wsu[G * D + tid] = T.M[tid], wsu[G * D + 8 + tid] = T.L[tid];
+        sync();                                    // the next query goes where o was
+        u = next;
+        fits = next_fits;
     }
 }
 
@@ -368,7 +439,7 @@ __global__ void __launch_bounds__(256) block_merge_kernel(BdArgs A) {
 
 cudaError_t launch_block_decode(const uint8_t *pool, const PoolGeom &geo, int layer, const float *q,
                                 const int32_t *page_table, int max_pages, const int32_t *plan,
-                                const kvq_plan_info &info, float *ws, int32_t *status, uint16_t *out_bf16,
+                                const kvq_plan_info &info, int n_ctas, float *ws, int32_t *status, uint16_t *out_bf16,
                                 float *out_f32, cudaStream_t s) {
     static std::mutex mu;
     static bool ready[64];
@@ -377,15 +448,19 @@ cudaError_t launch_block_decode(const uint8_t *pool, const PoolGeom &geo, int la
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!ready[dev]) {
-            const cudaError_t e = cudaFuncSetAttribute(block_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BD_SMEM);
+            cudaFuncAttributes fa;
+            cudaError_t e = cudaFuncGetAttributes(&fa, block_decode_kernel);
+            if (e != cudaSuccess) return e;
+            if (fa.numRegs != BD_REGS) return cudaErrorInvalidConfiguration;    // setmaxnreg.inc would wait for good
+            e = cudaFuncSetAttribute(block_decode_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BD_SMEM);
             if (e != cudaSuccess) return e;
             ready[dev] = true;
         }
     }
     const int n_q = info.n_kv_heads * info.group;
-    const BdArgs a{pool, geo, layer, q, page_table, max_pages, plan, info.n_units, info.n_seq, n_q, info.group, ws,
+    const BdArgs a{pool, geo, layer, q, page_table, max_pages, plan, info.n_units, n_ctas, info.n_seq, n_q, info.group, ws,
                    status, out_bf16, out_f32};
-    cudaError_t e = launch_ex(block_decode_kernel, dim3((unsigned)info.n_units), dim3(BD_THREADS), BD_SMEM, s, false, a);
+    cudaError_t e = launch_ex(block_decode_kernel, dim3((unsigned)n_ctas), dim3(BD_THREADS), BD_SMEM, s, false, a);
     if (e != cudaSuccess || !out_bf16 || info.n_units == info.n_seq * info.n_kv_heads) return e;
     return launch_ex(block_merge_kernel, dim3((unsigned)(info.n_seq * n_q)), dim3(256), 0, s, false, a);
 }

@@ -177,6 +177,8 @@ cudaError_t launch_ex(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sm
 // Plan (int32): [magic, n_units, n_seq, n_kv_heads, group, chunk, 0, 0]
 //               units[n_units][4] = {seq, kv_head, t_begin, t_end}
 //               start[n_seq * n_kv_heads + 1]  (first unit of each (seq, kv head))
+// fp8b: header entry 6 is n_ctas, and after start follow
+//               cta[n_ctas + 1]                (first unit of each CTA)
 // ---------------------------------------------------------------------------
 __host__ __device__ inline int plan_len_for(int n_units, int n_seq, int n_kv) {
     return PLAN_HEADER + 4 * n_units + n_seq * n_kv + 1;
@@ -391,7 +393,7 @@ cudaError_t launch_rope_append(int fmt, uint8_t *pool, const PoolGeom &geo, cons
 // Attention over an fp8b pool (kvq_block_decode.cu, kvq_block_prefill.cu).
 cudaError_t launch_block_decode(const uint8_t *pool, const PoolGeom &geo, int layer, const float *q,
                                 const int32_t *page_table, int max_pages, const int32_t *plan,
-                                const kvq_plan_info &info, float *ws, int32_t *status, uint16_t *out_bf16,
+                                const kvq_plan_info &info, int n_ctas, float *ws, int32_t *status, uint16_t *out_bf16,
                                 float *out_f32, cudaStream_t s);
 cudaError_t launch_block_prefill(const uint8_t *pool, const PoolGeom &geo, int layer, const void *q, int q_dtype,
                                  int64_t q_stride, const int32_t *page_table, int max_pages, const int32_t *plan,
