@@ -34,12 +34,11 @@ static_assert(BD_SETS * BD_REGS_COMPUTE + BD_REGS_REST <= 4 * BD_REGS, "the comp
 constexpr int BD_STAGES = 6;
 static_assert(BD_STAGES % BD_SETS == 0, "stages per set");
 constexpr uint64_t BD_WAIT_NS = 2000000000ull;
-constexpr int BD_OSTRIDE = 260;                   // floats of a head's row in the merge: heads 2t, 2t+1 of a store fall on their own banks
 constexpr int BD_RING = BD_STAGES * BT_BYTES;
 struct BdTail {                                   // after the ring
     union {
         uint4 q[16][32];                          // query fragments [k-step][lane], until a unit's last tile
-        float o[4][8][BD_OSTRIDE];                // merge of the warps, after it
+        float o[4][D][8];                         // merge of the warps [tile quarter][dim][head], after it
     };
     float scale[BD_STAGES][4];                    // the 16 bytes that hold the tile's scales
     float m[BD_WARPS][8], l[BD_WARPS][8], M[8], L[8], qscale[8];
@@ -95,8 +94,6 @@ __global__ void __launch_bounds__(BD_THREADS, 1) block_decode_kernel(BdArgs A) {
     }
     fence_mbar_init();
     __syncthreads();
-    // the merge kernel may take its place on the SMs now; it waits for this grid's end before it reads
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     grid_dependency_wait();
     const bool good = __ldg(A.plan) == PLAN_MAGIC && __ldg(A.plan + 1) == A.n_units && __ldg(A.plan + 2) == A.n_seq &&
                       __ldg(A.plan + 3) == A.geo.n_kv_heads && __ldg(A.plan + 6) == A.n_ctas;
@@ -350,25 +347,41 @@ __global__ void __launch_bounds__(BD_THREADS, 1) block_decode_kernel(BdArgs A) {
 #pragma unroll
                     for (int x = 0; x < 16; ++x)
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            float &to = T.o[w4][2 * t + (c & 1)][16 * x + g + 8 * (c >> 1)];
-                            to = turn == BD_SETS - 1 ? o[x][c] * f[c & 1] : fmaf(o[x][c], f[c & 1], to);
+                        for (int c = 0; c < 4; c += 2) {     // heads 2t, 2t + 1 of a dim
+                            float2 &to = *reinterpret_cast<float2 *>(&T.o[w4][16 * x + g + 4 * c][2 * t]);
+                            float2 v = turn == BD_SETS - 1 ? make_float2(0.f, 0.f) : to;
+                            v.x = fmaf(o[x][c], f[0], v.x);
+                            v.y = fmaf(o[x][c + 1], f[1], v.y);
+                            to = v;
                         }
                 sync();
             }
         }
         const int32_t *st = start + seq * A.geo.n_kv_heads + kvh;
         const bool whole = A.out_bf16 && __ldg(st) == i && __ldg(st + 1) == i + 1;
-        if (tid < D)
-            for (int h = 0; h < G; ++h) {
-                const float acc = (T.o[0][h][tid] + T.o[1][h][tid]) + (T.o[2][h][tid] + T.o[3][h][tid]);
+        if (tid < D) {
+            float acc[8];
+#pragma unroll
+            for (int h = 0; h < 8; h += 4) {
+                float4 v[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) v[w] = *reinterpret_cast<const float4 *>(&T.o[w][tid][h]);
+                acc[h] = (v[0].x + v[1].x) + (v[2].x + v[3].x);
+                acc[h + 1] = (v[0].y + v[1].y) + (v[2].y + v[3].y);
+                acc[h + 2] = (v[0].z + v[1].z) + (v[2].z + v[3].z);
+                acc[h + 3] = (v[0].w + v[1].w) + (v[2].w + v[3].w);
+            }
+#pragma unroll
+            for (int h = 0; h < 8; ++h) {
+                if (h >= G) break;
                 if (whole) {
                     const float L = T.L[h];
-                    write_out(A, (int64_t)seq * A.n_q_heads + kvh * G + h, tid, L > 0.0f ? acc / L : 0.0f);
+                    write_out(A, (int64_t)seq * A.n_q_heads + kvh * G + h, tid, L > 0.0f ? acc[h] / L : 0.0f);
                 } else {
-                    wsu[h * D + tid] = acc;
+                    wsu[h * D + tid] = acc[h];
                 }
             }
+        }
         if (!whole && tid < G) wsu[G * D + tid] = T.M[tid], wsu[G * D + 8 + tid] = T.L[tid];
         sync();                                    // the next query goes where o was
         u = next;
@@ -376,63 +389,118 @@ __global__ void __launch_bounds__(BD_THREADS, 1) block_decode_kernel(BdArgs A) {
     }
 }
 
-// Merge of the units of one (sequence, query head): M = max m_u, L = sum l_u
-// 2^(m_u - M), o = sum 2^(m_u - M) o_u / L, a head of four 64-lane parts.
-__global__ void __launch_bounds__(256) block_merge_kernel(BdArgs A) {
-    __shared__ float4 part[4][64];
-    __shared__ float s_l[8], s_m[8];
+// Merge of the units of one (sequence, KV head): M = max m_u, L = sum l_u
+// 2^(m_u - M), o = sum 2^(m_u - M) o_u / L for each of its heads.  A CTA takes
+// 256 / SPLIT dims of all eight heads; a thread four dims of one head and every
+// PARTS-th unit.  It asks for its first units' partials before it knows their
+// weights, so a merge is two loads deep (the unit range, then everything else).
+constexpr int BM_THREADS = 512;
+constexpr int BM_BATCH = 5;                        // units of a thread loaded together
+template <int SPLIT> __global__ void __launch_bounds__(BM_THREADS) block_merge_kernel(BdArgs A) {
+    constexpr int COLS = D / SPLIT / 4, PARTS = BM_THREADS / 8 / COLS, CHUNK = 128;
+    static_assert(PARTS * COLS * 8 == BM_THREADS, "threads");
+    __shared__ float4 part[PARTS][8][COLS];
+    __shared__ float s_f[CHUNK][8], s_M[8], s_L[8], s_old[8];
     grid_dependency_wait();
-    const int tid = threadIdx.x, G = A.G;
-    const int row = blockIdx.x, seq = row / A.n_q_heads, hq = row - seq * A.n_q_heads, kvh = hq / G, h = hq - kvh * G;
-    const int32_t *start = A.plan + PLAN_HEADER + 4 * A.n_units + seq * A.geo.n_kv_heads + kvh;
-    const int u0 = start[0], u1 = start[1];
-    if (u0 < 0 || u1 > A.n_units || u1 <= u0) {
+    const int tid = threadIdx.x, G = A.G, lane = tid & 31, warp = tid >> 5;
+    const int grp = blockIdx.x / SPLIT, seq = grp / A.geo.n_kv_heads, kvh = grp - seq * A.geo.n_kv_heads;
+    const int32_t *start = A.plan + PLAN_HEADER + 4 * (int64_t)A.n_units + grp;
+    const int u0 = __ldg(start), u1 = __ldg(start + 1), n = u1 - u0;
+    if (u0 < 0 || u1 > A.n_units || n <= 0) {
         if (tid == 0) status_or(A.status, KVQ_STATUS_BAD_PLAN);
         return;
     }
-    if (u1 - u0 == 1 && A.plan[1] == A.n_units) return;      // the unit wrote the output itself
-    const int stride = ws_unit_floats(G);
-    const float *ws = A.ws;
-    float M = -INFINITY;
-    for (int x = u0 + tid; x < u1; x += 256) M = fmaxf(M, ws[(int64_t)x * stride + G * D + h]);
-#pragma unroll
-    for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    if ((tid & 31) == 0) s_m[tid >> 5] = M;
-    __syncthreads();
-#pragma unroll
-    for (int x = 0; x < 8; ++x) M = fmaxf(M, s_m[x]);
-    const int c = tid & 63, pt = tid >> 6;
+    if (n == 1) return;                            // the unit wrote the output itself
+    const int c = tid % COLS, h = tid / COLS % 8, pt = tid / COLS / 8;
+    const int64_t stride = ws_unit_floats(G);
+    const float *ws = A.ws + u0 * stride, *mine = ws + min(h, G - 1) * D + (blockIdx.x % SPLIT) * (D / SPLIT) + 4 * c;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float L = 0.0f;
-#pragma unroll 8
-    for (int x = u0 + pt; x < u1; x += 4) {
-        const float *p = ws + (int64_t)x * stride;
-        const float mu = p[G * D + h], f = mu == -INFINITY ? 0.0f : exp2f(mu - M);
-        const float4 v = *reinterpret_cast<const float4 *>(p + h * D + 4 * c);
-        acc.x = fmaf(v.x, f, acc.x);
-        acc.y = fmaf(v.y, f, acc.y);
-        acc.z = fmaf(v.z, f, acc.z);
-        acc.w = fmaf(v.w, f, acc.w);
-        L = fmaf(p[G * D + 8 + h], f, L);
-    }
-    part[pt][c] = acc;
-    if (c == 0) s_l[pt] = L;
-    __syncthreads();
-    if (tid < 64) {
-        L = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
-        const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-        float x[4] = {0.f, 0.f, 0.f, 0.f};
+    if (tid < 8) s_M[tid] = -INFINITY, s_L[tid] = 0.0f;
+    for (int c0 = 0; c0 < n; c0 += CHUNK) {        // 128 units at a time
+        const int nc = min(CHUNK, n - c0);
+        float4 v[BM_BATCH];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 v = part[i][c];
-            x[0] += v.x;
-            x[1] += v.y;
-            x[2] += v.z;
-            x[3] += v.w;
+        for (int b = 0; b < BM_BATCH; ++b) {
+            const int x = pt + PARTS * b;
+            v[b] = x < nc ? *reinterpret_cast<const float4 *>(mine + (c0 + x) * stride) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
+        if (warp < G) {                            // head `warp`: the reference, the units' factors, the sum
+            float m[CHUNK / 32], l[CHUNK / 32];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) write_out(A, row, 4 * c + i, x[i] * inv);
+            for (int x = 0; x < CHUNK / 32; ++x) {
+                const float *p = ws + (c0 + lane + 32 * x) * stride + G * D + warp;
+                m[x] = lane + 32 * x < nc ? p[0] : -INFINITY;
+                l[x] = lane + 32 * x < nc ? p[8] : 0.0f;
+            }
+            __syncwarp();
+            const float M0 = c0 ? s_M[warp] : -INFINITY;
+            float M = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+#pragma unroll
+            for (int d = 16; d; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+            M = fmaxf(M, M0);
+            float L = 0.0f;
+#pragma unroll
+            for (int x = 0; x < CHUNK / 32; ++x) {
+                const float f = m[x] == -INFINITY ? 0.0f : exp2f(m[x] - M);
+                if (lane + 32 * x < nc) s_f[lane + 32 * x][warp] = f;
+                L = fmaf(l[x], f, L);
+            }
+#pragma unroll
+            for (int d = 16; d; d >>= 1) L += __shfl_xor_sync(0xffffffffu, L, d);
+            if (lane == 0) {
+                const float old = M0 == -INFINITY ? 0.0f : exp2f(M0 - M);
+                s_old[warp] = old;
+                s_L[warp] = fmaf(c0 ? s_L[warp] : 0.0f, old, L);
+                s_M[warp] = M;
+            }
+        }
+        __syncthreads();
+        if (c0 > 0 && h < G) {
+            const float old = s_old[h];
+            acc.x *= old;
+            acc.y *= old;
+            acc.z *= old;
+            acc.w *= old;
+        }
+        for (int b0 = 0; b0 < nc; b0 += PARTS * BM_BATCH) {
+            if (b0 > 0)
+#pragma unroll
+                for (int b = 0; b < BM_BATCH; ++b) {
+                    const int x = b0 + pt + PARTS * b;
+                    v[b] = x < nc ? *reinterpret_cast<const float4 *>(mine + (c0 + x) * stride) : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+#pragma unroll
+            for (int b = 0; b < BM_BATCH; ++b) {
+                const int x = b0 + pt + PARTS * b;
+                const float w = x < nc && h < G ? s_f[x][h] : 0.0f;
+                acc.x = fmaf(v[b].x, w, acc.x);
+                acc.y = fmaf(v[b].y, w, acc.y);
+                acc.z = fmaf(v[b].z, w, acc.z);
+                acc.w = fmaf(v[b].w, w, acc.w);
+            }
+        }
+        __syncthreads();
     }
+    if (PARTS > 1) {
+        part[pt][h][c] = acc;
+        __syncthreads();
+        if (pt > 0) return;
+#pragma unroll
+        for (int x = 1; x < PARTS; ++x) {          // the parts in order
+            const float4 v = part[x][h][c];
+            acc.x += v.x;
+            acc.y += v.y;
+            acc.z += v.z;
+            acc.w += v.w;
+        }
+    }
+    if (h >= G) return;
+    const float inv = s_L[h] > 0.0f ? 1.0f / s_L[h] : 0.0f;
+    const int64_t at = ((int64_t)seq * A.n_q_heads + kvh * G + h) * D + (blockIdx.x % SPLIT) * (D / SPLIT) + 4 * c;
+    const float4 o = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), b = __floats2bfloat162_rn(o.z, o.w);
+    *reinterpret_cast<uint2 *>(A.out_bf16 + at) = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    if (A.out_f32) *reinterpret_cast<float4 *>(A.out_f32 + at) = o;
 }
 
 }  // namespace
@@ -462,7 +530,12 @@ cudaError_t launch_block_decode(const uint8_t *pool, const PoolGeom &geo, int la
                    status, out_bf16, out_f32};
     cudaError_t e = launch_ex(block_decode_kernel, dim3((unsigned)n_ctas), dim3(BD_THREADS), BD_SMEM, s, false, a);
     if (e != cudaSuccess || !out_bf16 || info.n_units == info.n_seq * info.n_kv_heads) return e;
-    return launch_ex(block_merge_kernel, dim3((unsigned)(info.n_seq * n_q)), dim3(256), 0, s, false, a);
+    // few ranges, each cut into many units, are merged by 16 or 4 CTAs each, many by one: as many as fit the 148 SMs at once
+    // (1 x 32,768 tokens of four KV heads: 21.3 us with 4, 20.1 with 16; 48 ragged sequences of two: 54 us with 4, 48 with 1)
+    const int groups = info.n_seq * info.n_kv_heads;
+    if (groups <= 148 / 16) return launch_ex(block_merge_kernel<16>, dim3((unsigned)groups * 16), dim3(BM_THREADS), 0, s, false, a);
+    if (groups <= 148 / 4) return launch_ex(block_merge_kernel<4>, dim3((unsigned)groups * 4), dim3(BM_THREADS), 0, s, false, a);
+    return launch_ex(block_merge_kernel<1>, dim3((unsigned)groups), dim3(BM_THREADS), 0, s, false, a);
 }
 
 }  // namespace kvq
