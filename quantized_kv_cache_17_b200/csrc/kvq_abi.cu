@@ -73,10 +73,12 @@ int check_pool(const kvq_pool *pool, int layer, PoolGeom *geo) {
 // merge moves as many bytes as four steps read).
 constexpr int64_t PFB_TILE_COST = 8, PFB_MIN_PART = 4;
 
-// Decode plan of fp8b: what a unit costs beyond its steps of 64 tokens (query,
-// merge of the warps, result: about 1.5 us, 0.75 us a step) and the shortest unit
-// worth cutting off.
-constexpr int64_t BD_UNIT_COST = 2, BD_MIN_PART = 2;
+// Decode plan of fp8b: what a unit costs beyond its steps of 64 tokens, in steps
+// (its query, the merge of its warps, its result and its share of the units' merge;
+// 48 ragged sequences took 50, 48, 45, 41, 39.6, 40.2 and 41 us planned with 1, 2,
+// 3, 4, 6, 8 and 10, 32,768 tokens 21.1, 20.1, 19.7 and from 4 on 19.2), and the
+// shortest unit worth cutting off.
+constexpr int64_t BD_UNIT_COST = 6, BD_MIN_PART = 2;
 
 // The (sequence, KV head) ranges one after another, cut where a CTA has its share,
 // so that a CTA takes consecutive units and all CTAs about the same; the units
