@@ -52,6 +52,15 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
     return r;
 }
 
+// Four E4M3 bytes to two fp16 pairs, exact.  The halves of the word go to the
+// conversions as they are: masked and shifted out one by one (e4m3x2_to_h2) they
+// cost as many instructions as the conversions.
+__device__ __forceinline__ void e4m3x4_to_h2(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+
 __device__ __forceinline__ int block_k_off(int t, int d) {
     return (d >> 7) * 8192 + (t >> 3) * 1024 + (t & 7) * 128 + ((((d >> 4) & 7) ^ (t & 7)) << 4) + (d & 15);
 }

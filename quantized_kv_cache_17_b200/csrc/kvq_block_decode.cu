@@ -255,8 +255,11 @@ __global__ void __launch_bounds__(BD_THREADS, 1) block_decode_kernel(BdArgs A) {
                             const uint4 w = lds128(&T.q[8 * h + 4 * ii + x][lane]);
                             const uint32_t q[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                            for (int y = 0; y < 2; ++y)
-                                mma16816(sc[y][h], q, e4m3x2_to_h2(kw[y][h][x] & 0xFFFFu), e4m3x2_to_h2(kw[y][h][x] >> 16));
+                            for (int y = 0; y < 2; ++y) {
+                                uint32_t b0, b1;
+                                e4m3x4_to_h2(kw[y][h][x], b0, b1);
+                                mma16816(sc[y][h], q, b0, b1);
+                            }
                         }
                 }
                 // scores of head g, tokens 4t .. 4t + 3: high and low rows, both dim halves
@@ -306,7 +309,9 @@ __global__ void __launch_bounds__(BD_THREADS, 1) block_decode_kernel(BdArgs A) {
                     // dims 16 x + g and + 8: rows of V; (dim >> 1) & 3 = (g >> 1) & 3 for both
                     const uint8_t *vr = vt + x * 1024 + g * 64 + ((w4 ^ ((g >> 1) & 3)) << 4) + 4 * t;
                     const uint32_t va = lds32(vr) & keep, vb = lds32(vr + 512) & keep;
-                    const uint32_t a[4] = {e4m3x2_to_h2(va & 0xFFFFu), e4m3x2_to_h2(vb & 0xFFFFu), e4m3x2_to_h2(va >> 16), e4m3x2_to_h2(vb >> 16)};
+                    uint32_t a[4];
+                    e4m3x4_to_h2(va, a[0], a[2]);
+                    e4m3x4_to_h2(vb, a[1], a[3]);
                     mma16816(o[x], a, whi[0], whi[1]);
                     mma16816(o[x], a, wlo[0], wlo[1]);
                 }
