@@ -82,6 +82,16 @@ class PrefillInfo(ctypes.Structure):
 
 
 _lib = None
+_torch_module = None
+
+
+def _torch():
+    """torch, imported at the first call that needs it."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def lib():
@@ -142,7 +152,7 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
+        torch = _torch()
         if torch.cuda.is_initialized():              # the same handle, without building a Stream object (3 us a call)
             return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
@@ -325,7 +335,7 @@ def paged_decode_attn_fp8b(pool, layer, q, page_table, plan_dev, info, workspace
 
 def _dtype(t, what: str) -> int:
     """The kvq_dtype of a torch element type."""
-    import torch
+    torch = _torch()
     d = 0 if t is torch.float32 else 1 if t is torch.bfloat16 else 2 if t is torch.float16 else None
     if d is None:
         raise KVQError(f"{what}: {t} is not float32, bfloat16 or float16")
@@ -342,7 +352,7 @@ def _rows(t, heads: int, what: str) -> int:
 
 def _index(t, what: str) -> int:
     """Address of a contiguous int32 tensor."""
-    import torch
+    torch = _torch()
     if t.dtype is not torch.int32 or not t.is_contiguous():
         raise KVQError(f"{what} is not a contiguous int32 tensor")
     return t.data_ptr()
@@ -350,7 +360,7 @@ def _index(t, what: str) -> int:
 
 def _on_current_device(what: str, *tensors):
     """The kernels are launched on the current device: every tensor of the call has to be there."""
-    import torch
+    torch = _torch()
     dev = torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
     for t in tensors:
         if t is not None and t.get_device() != dev:
@@ -368,7 +378,7 @@ def kv_append_rope(pool: KVPool, layer: int, k, v, row_start, pos0, page_table, 
     type q_out_dtype: fp32, or q's own type for fp8b pools; by default fp32 except
     that fp8b keeps q's type; rows past row_start[-1] are not written), None without
     q.  k and v may both be None."""
-    import torch
+    torch = _torch()
     d = pool.desc
     first = k if k is not None else q
     if first is None or (k is None) != (v is None):

@@ -69,9 +69,9 @@ int check_pool(const kvq_pool *pool, int layer, PoolGeom *geo) {
 // Prefill plan: what a part of a row tile costs beyond its steps of 128 keys, in
 // steps (its query, its output and the rescaling of its first steps; a 7,777-token
 // prompt took 949, 811, 780 and 765 us planned with 3, 5, 7 and 9, 512 tokens at
-// 32,768 386, 384, 369 and 366), and the shortest part worth a partial result (its
-// merge moves as many bytes as four steps read).
-constexpr int64_t PFB_TILE_COST = 8, PFB_MIN_PART = 4;
+// 32,768 386, 384, 369 and 366), and the shortest part worth a partial result (8 x 5
+// tokens at 64 to 4,095 keys: 27.3, 28.7, 29.0, 31.8 and 34.4 us with 1, 2, 3, 4 and 6).
+constexpr int64_t PFB_TILE_COST = 8, PFB_MIN_PART = 2;
 
 // Decode plan of fp8b: what a unit costs beyond its steps of 64 tokens, in steps
 // (its query, the merge of its warps, its result and its share of the units' merge;

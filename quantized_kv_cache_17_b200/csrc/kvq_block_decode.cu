@@ -95,12 +95,13 @@ __global__ void __launch_bounds__(BD_THREADS, 1) block_decode_kernel(BdArgs A) {
     fence_mbar_init();
     __syncthreads();
     grid_dependency_wait();
+    const int32_t *start = A.plan + PLAN_HEADER + 4 * (int64_t)A.n_units;
+    const int32_t *cta = start + A.n_seq * A.geo.n_kv_heads + 1 + blockIdx.x;
+    const int first = __ldg(cta), last = __ldg(cta + 1);             // together with the header: one wait
     const bool good = __ldg(A.plan) == PLAN_MAGIC && __ldg(A.plan + 1) == A.n_units && __ldg(A.plan + 2) == A.n_seq &&
                       __ldg(A.plan + 3) == A.geo.n_kv_heads && __ldg(A.plan + 6) == A.n_ctas;
     if (!good && tid == 0) status_or(A.status, KVQ_STATUS_BAD_PLAN);
-    const int32_t *start = A.plan + PLAN_HEADER + 4 * (int64_t)A.n_units;
-    const int32_t *cta = start + A.n_seq * A.geo.n_kv_heads + 1;
-    const int i0 = good ? max(0, __ldg(cta + blockIdx.x)) : 0, i1 = good ? min(A.n_units, __ldg(cta + blockIdx.x + 1)) : 0;
+    const int i0 = good ? max(0, first) : 0, i1 = good ? min(A.n_units, last) : 0;
 
     if (warp >= BD_WARPS) {                        // ---- copies ----
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(BD_REGS_REST));

@@ -254,9 +254,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
     tc_fence_after();
     const uint32_t tmem = X.tmem;
     grid_dependency_wait();
+    const int32_t *start = A.plan + PLAN_HEADER + (int64_t)A.n_units * PFB_UNIT + (int64_t)A.n_merges * PFB_MERGE + blockIdx.x;
+    const int first = __ldg(start), last = __ldg(start + 1);         // together with the header: one wait
     const bool good = plan_ok(A);
-    const int32_t *start = A.plan + PLAN_HEADER + (int64_t)A.n_units * PFB_UNIT + (int64_t)A.n_merges * PFB_MERGE;
-    const int i0 = good ? max(0, start[blockIdx.x]) : 0, i1 = good ? min(A.n_units, start[blockIdx.x + 1]) : 0;
+    const int i0 = good ? max(0, first) : 0, i1 = good ? min(A.n_units, last) : 0;
     // A wait that gives up (2 s, or another role's did) raises the CTA's flag and the call's status.  From then on
     // nothing is copied or multiplied and no wait waits, but every role walks its loop to the end: the warps' own
     // barriers always find their partners.  Called by whole warps.
