@@ -263,6 +263,8 @@ def paged_decode_attn_combined(pool: KVPool, layer: int, q, page_table, plan_dev
                                out_bf16, out_f32=None, status=None, stream=None):
     """Decode with the combine fused in; workspace must have been zero-filled
     once before its first use (the call leaves its counters at zero)."""
+    if pool.fmt == FP8B:
+        _on_current_device("paged_decode_attn_fp8b_combined", pool.buf, q, page_table, plan_dev, workspace, out_bf16, out_f32, status)
     cp = pool.c_pool()
     name = _DECODE[pool.fmt] + "_combined"
     _check(getattr(lib(), name)(ctypes.byref(cp), layer, _ptr(q), _ptr(page_table), page_table.shape[1],
@@ -293,6 +295,8 @@ def paged_decode_attn(pool: KVPool, layer: int, q, page_table, plan_dev, info: P
                       stream=None, cudacore: bool = False):
     """Split-K decode attention of the pool's format (tensor-core kernel, or
     the CUDA-core control when cudacore=True); partials go to workspace."""
+    if pool.fmt == FP8B:
+        _on_current_device("paged_decode_attn_fp8b", pool.buf, q, page_table, plan_dev, workspace, status)
     cp = pool.c_pool()
     args = (ctypes.byref(cp), layer, _ptr(q), _ptr(page_table), page_table.shape[1], _ptr(plan_dev),
             ctypes.byref(info), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
@@ -413,7 +417,7 @@ def kv_append_rope(pool: KVPool, layer: int, k, v, row_start, pos0, page_table, 
         if cos_sin.dtype is not torch.float32 or not cos_sin.is_contiguous():
             raise KVQError("kv_append_rope: cos_sin is not a contiguous float32 tensor")
         cp_ = cos_sin.data_ptr()
-    _on_current_device("kv_append_rope", first, v, q, q_out, row_start, pos0, page_table, cos_sin, status)
+    _on_current_device("kv_append_rope", pool.buf, first, v, q, q_out, row_start, pos0, page_table, cos_sin, status)
     cp = pool.c_pool()
     _check(lib().kv_append_rope(ctypes.byref(cp), layer, cp_, n_pos, rot, 1 if interleaved else 0, qp, kp, vp, dt, qs, ks, vs,
                                 n_rows, rs, p0, pt, max_pages, n_seq, op, odt, _ptr(status), _stream(stream)),
@@ -457,7 +461,7 @@ def paged_prefill_attn_fp8b(pool: KVPool, layer: int, q, page_table, plan_dev, i
     pt, pl = _index(page_table, "page_table"), _index(plan_dev, "plan_dev")
     if plan_dev.shape[0] < info.plan_len:
         raise KVQError(f"{what}: plan_dev is shorter than the plan")
-    _on_current_device(what, q, page_table, plan_dev, workspace, out_bf16, out_f32, status)
+    _on_current_device(what, pool.buf, q, page_table, plan_dev, workspace, out_bf16, out_f32, status)
     cp = pool.c_pool()
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().paged_prefill_attn_fp8b(ctypes.byref(cp), layer, q.data_ptr(), _dtype(q.dtype, what), qs, pt,

@@ -510,6 +510,7 @@ int kv_append_rope(const kvq_pool *pool, int layer, const float *cos_sin, int n_
     if (n_rows < 0 || n_seq <= 0 || max_pages <= 0 || (int64_t)max_pages * PAGE > INT32_MAX) return KVQ_EINVAL;
     if (rot_dim < 0 || rot_dim > D || rot_dim % 16 != 0 || (interleaved != 0 && interleaved != 1)) return KVQ_EINVAL;
     if (dtype < KVQ_F32 || dtype > KVQ_F16) return KVQ_EINVAL;
+    if (n_rows == 0) return KVQ_OK;
     if (!k != !v || (!k && !q) || !q != !q_out) return KVQ_EINVAL;
     if (q && q_dtype != KVQ_F32 && q_dtype != dtype) return KVQ_EINVAL;
     if (q && q_dtype != KVQ_F32 && pool->desc.fmt != KVQ_FP8B) return KVQ_EUNSUPPORTED;   // those decodes take fp32
@@ -522,7 +523,6 @@ int kv_append_rope(const kvq_pool *pool, int layer, const float *cos_sin, int n_
     if ((k && (k_stride < (int64_t)geo.n_kv_heads * D || v_stride < (int64_t)geo.n_kv_heads * D)) ||
         (q && q_stride < (int64_t)n_q * D))
         return KVQ_EINVAL;
-    if (n_rows == 0) return KVQ_OK;
     if (!row_start || !pos0 || !page_table) return KVQ_EINVAL;
     const int64_t esize = dtype == KVQ_F32 ? 4 : 2;
     if ((rot_dim && !aligned16(cos_sin)) || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||

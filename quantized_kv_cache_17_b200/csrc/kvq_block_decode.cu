@@ -278,7 +278,8 @@ __global__ void __launch_bounds__(BD_THREADS, 1) block_decode_kernel(BdArgs A) {
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 const int ev = dv > 0.0f ? (int)(__float_as_uint(dv) >> 23) - 127 : -10000;
                 if (__any_sync(0xffffffffu, mx > m + 8.0f) || ev > E) {
-                    const float mn = fmaxf(m, mx), fm = m == -INFINITY ? 0.0f : exp2f(m - mn);
+                    const float mn = mx > m + 8.0f ? mx : m;      // only heads that ask move
+                    const float fm = m == mn ? 1.0f : (m == -INFINITY ? 0.0f : exp2f(m - mn));
                     const float fe = ev > E ? pow2i(E - ev) : 1.0f;
                     m = mn;
                     E = max(E, ev);
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(BD_THREADS, 1) block_decode_kernel(BdArgs A) {
                 if (h >= G) break;
                 if (whole) {
                     const float L = T.L[h];
-                    write_out(A, (int64_t)seq * A.n_q_heads + kvh * G + h, tid, L > 0.0f ? acc[h] / L : 0.0f);
+                    write_out(A, (int64_t)seq * A.n_q_heads + kvh * G + h, tid, L == 0.0f ? 0.0f : acc[h] / L);   // NaN stays NaN
                 } else {
                     wsu[h * D + tid] = acc[h];
                 }
@@ -501,7 +502,7 @@ template <int SPLIT> __global__ void __launch_bounds__(BM_THREADS) block_merge_k
         }
     }
     if (h >= G) return;
-    const float inv = s_L[h] > 0.0f ? 1.0f / s_L[h] : 0.0f;
+    const float inv = s_L[h] == 0.0f ? 0.0f : 1.0f / s_L[h];
     const int64_t at = ((int64_t)seq * A.n_q_heads + kvh * G + h) * D + (blockIdx.x % SPLIT) * (D / SPLIT) + 4 * c;
     const float4 o = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), b = __floats2bfloat162_rn(o.z, o.w);

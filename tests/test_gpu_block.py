@@ -186,6 +186,21 @@ def test_append_many_sequences():
     run_appends([toks], 2, 1, torch.bfloat16, 64, False, False, [max(t, 1) for t in toks], 9)
 
 
+def test_append_decoding_batch_with_padding():
+    """Fewer rows than tiles they could touch (a tile belongs to its first row), sequences without rows, padding behind."""
+    run_appends([[1, 0, 2, 1, 70], [1, 1, 0, 63, 1], [1, 1, 1, 1, 1]], 6, 2, torch.bfloat16, 64, False, True, [9, 9, 9, 80, 90], 12, pad=6)
+    run_appends([[1] * 40, [2] * 40], 4, 1, torch.float16, 32, True, False, [3] * 40, 13, pad=2)
+
+
+def test_append_of_no_rows():
+    pool = make_pool(br.Cache(2, 2), 4)
+    before = pool.buf.clone()
+    k, q = torch.empty((0, 2, 256), device="cuda"), torch.empty((0, 4, 256), device="cuda")
+    out = kvq.kv_append_rope(pool, 0, k, k, i32([0, 0, 0]), i32([5, 0]), i32([[0], [1]]), q=q)
+    torch.cuda.synchronize()
+    assert tuple(out.shape) == (0, 4, 256) and torch.equal(pool.buf, before)
+
+
 def test_append_q_only_and_kv_only_and_in_place():
     rng = np.random.default_rng(4)
     table, n_slots = page_table(rng, [300])
@@ -543,6 +558,30 @@ def test_prefill_bad_slots_and_plans():
         assert int(status.item()) & kvq.STATUS_BAD_PLAN, (at, value)
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_nonfinite_queries_stay_in_their_rows(bad):
+    rng = np.random.default_rng(95)
+    lens, pos0, toks = [700], [660], [40]
+    table, n_slots = page_table(rng, lens)
+    cache = random_cache(rng, n_slots, 1)
+    pool = make_pool(cache, 4)
+    q = rng.standard_normal((40, 4, 256)).astype(np.float32)
+    spoilt = q.copy()
+    spoilt[7, 2, 100] = bad
+    for n_ctas in (1, 148):
+        out, of = prefill(pool, dev(spoilt, torch.bfloat16), dev(table), pos0, toks, n_ctas=n_ctas)
+        want, wf = prefill(pool, dev(q, torch.bfloat16), dev(table), pos0, toks, n_ctas=n_ctas)
+        assert torch.isnan(of[7, 2]).all() and torch.isnan(out[7, 2]).all()
+        # the rows of a warp move their references together, so the others are as near, not the same bits
+        of[7, 2], out[7, 2] = wf[7, 2], want[7, 2]
+        check_prefill(cache, table, pos0, toks, dev(q, torch.bfloat16), out, of, torch.bfloat16)
+        a, af = decode(pool, dev(spoilt[7:8]), dev(table), lens, n_ctas=n_ctas)
+        b, bf = decode(pool, dev(q[7:8]), dev(table), lens, n_ctas=n_ctas)
+        assert torch.isnan(af[0, 2]).all()
+        af[0, 2] = bf[0, 2]
+        assert torch.equal(af, bf)
+
+
 # ---- together --------------------------------------------------------------
 def test_serving_run_of_the_operators():
     """Prompts in two chunks, then decoding steps: append (rotated), prefill and decode as a server calls them, in one captured
@@ -600,6 +639,94 @@ def test_serving_run_of_the_operators():
         check_decode(cache_now(), table, now, qf.cpu().numpy(), out, of)
         pos = now
     assert int(status.item()) == 0
+
+
+def test_calls_side_by_side_on_two_streams():
+    """Two batches with workspaces of their own, on two streams at once, give what they give alone."""
+    rng = np.random.default_rng(120)
+    state = []
+    for lens in ([3000, 40], [1234]):
+        table, n_slots = page_table(rng, lens)
+        cache = random_cache(rng, n_slots, 2)
+        pool = make_pool(cache, 12)
+        plan, info = kvq.decode_plan(pool.desc, lens, table.shape[1])
+        pplan, pinfo = kvq.prefill_plan(pool.desc, [n - 30 for n in lens], [30] * len(lens), table.shape[1])
+        state.append(dict(pool=pool, table=dev(table), q=dev(rng.standard_normal((len(lens), 12, 256)).astype(np.float32)),
+                          pq=dev(rng.standard_normal((30 * len(lens), 12, 256)).astype(np.float32), torch.bfloat16), plan=dev(plan), info=info,
+                          pplan=dev(pplan), pinfo=pinfo, stream=torch.cuda.Stream()))
+
+    def go(s):
+        ws = torch.empty(s["info"].workspace_bytes // 4, device="cuda")
+        pws = torch.empty(max(1, s["pinfo"].workspace_bytes // 4), device="cuda")
+        o, po = (torch.empty(s[n].shape, dtype=torch.bfloat16, device="cuda") for n in ("q", "pq"))
+        for _ in range(4):
+            kvq.paged_decode_attn_combined(s["pool"], 0, s["q"], s["table"], s["plan"], s["info"], ws, o)
+            kvq.paged_prefill_attn_fp8b(s["pool"], 0, s["pq"], s["table"], s["pplan"], s["pinfo"], pws, po)
+        return o, po
+
+    alone = [go(s) for s in state]
+    torch.cuda.synchronize()
+    both = []
+    for s in state:
+        with torch.cuda.stream(s["stream"]):
+            both.append(go(s))
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_offsets_past_32_bits():
+    """A pool of 5.5 GB whose last pages hold the sequence, in its second layer."""
+    rng = np.random.default_rng(130)
+    slots, lens = 10500, [600]
+    table = np.array([[slots - 1, slots - 3, slots - 2]], np.int32)
+    cs = dev(br.rope_table(700, 64))
+    pool = kvq.KVPool.allocate(kvq.make_desc(2, 2, 12, slots, "fp8b"))
+    assert kvq.pool_bytes(pool.desc) > 5 << 30
+    x = dev(rng.standard_normal((600, 16, 256)).astype(np.float32), torch.bfloat16)
+    q = kvq.kv_append_rope(pool, 1, x[:, 12:14], x[:, 14:], i32([0, 600]), i32([0]), dev(table), cos_sin=cs, q=x[:, :12])
+    view = pool.buf.view(2, slots, 2, br.PAGE_BYTES)
+    assert not view[0].any() and not view[1, :slots - 3].any()
+    cache = br.Cache.unpack(view[1, slots - 3:].cpu().numpy())
+    near = table - (slots - 3)
+    model = br.Cache(3, 2)
+    model.append(near[0], 0, br.rotate(x[:, 12:14].float().cpu().numpy(), np.arange(600), br.rope_table(700, 64), False),
+                 x[:, 14:].float().cpu().numpy())
+    assert np.array_equal(model.pack(), cache.pack())
+    plan, info = kvq.prefill_plan(pool.desc, [590], [10], 3)
+    ws = torch.empty(max(1, info.workspace_bytes // 4), device="cuda")
+    out, of = torch.empty((10, 12, 256), dtype=torch.bfloat16, device="cuda"), torch.empty((10, 12, 256), device="cuda")
+    kvq.paged_prefill_attn_fp8b(pool, 1, q[590:], dev(table), dev(plan), info, ws, out, of)
+    check_prefill(cache, near, [590], [10], q[590:], out, of, torch.bfloat16)
+    plan, info = kvq.decode_plan(pool.desc, lens, 3)
+    ws = torch.empty(info.workspace_bytes // 4, device="cuda")
+    out, of = torch.empty((1, 12, 256), dtype=torch.bfloat16, device="cuda"), torch.empty((1, 12, 256), device="cuda")
+    kvq.paged_decode_attn_combined(pool, 1, q[599:].float(), dev(table), dev(plan), info, ws, out, of)
+    check_decode(cache, near, lens, q[599:].float().cpu().numpy(), out, of)
+
+
+def test_prefill_replayed_from_a_graph():
+    """Captured once, replayed with other queries and another page order."""
+    rng = np.random.default_rng(140)
+    pos0, toks = [300, 0], [70, 150]
+    lens = [p + t for p, t in zip(pos0, toks)]
+    table, n_slots = page_table(rng, lens)
+    cache = random_cache(rng, n_slots, 2)
+    pool = make_pool(cache, 12)
+    plan, info = kvq.prefill_plan(pool.desc, pos0, toks, table.shape[1])
+    pd, ws, td = dev(plan), torch.empty(max(1, info.workspace_bytes // 4), device="cuda"), dev(table)
+    q = torch.zeros((sum(toks), 12, 256), dtype=torch.bfloat16, device="cuda")
+    out, of = torch.empty_like(q), torch.empty(q.shape, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        kvq.paged_prefill_attn_fp8b(pool, 0, q, td, pd, info, ws, out, of)
+    for seed in range(2):
+        q.copy_(dev(rng.standard_normal(tuple(q.shape)).astype(np.float32), torch.bfloat16))
+        table = np.where(table >= 0, (table + 1) % n_slots, table).astype(np.int32)
+        td.copy_(dev(table))
+        graph.replay()
+        torch.cuda.synchronize()
+        check_prefill(cache, table, pos0, toks, q, out, of, torch.bfloat16)
 
 
 def test_fp8b_pages_move_through_the_resident_cache():
