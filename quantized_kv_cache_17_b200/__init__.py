@@ -337,27 +337,33 @@ def paged_decode_attn_fp8b(pool, layer, q, page_table, plan_dev, info, workspace
     paged_decode_attn(pool, layer, q, page_table, plan_dev, info, workspace, status, stream)
 
 
+_dtypes = {}                      # torch element type -> kvq_dtype, filled at the first use
+
+
 def _dtype(t, what: str) -> int:
     """The kvq_dtype of a torch element type."""
-    torch = _torch()
-    d = 0 if t is torch.float32 else 1 if t is torch.bfloat16 else 2 if t is torch.float16 else None
+    d = _dtypes.get(t)
     if d is None:
-        raise KVQError(f"{what}: {t} is not float32, bfloat16 or float16")
+        torch = _torch()
+        _dtypes.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2})
+        d = _dtypes.get(t)
+        if d is None:
+            raise KVQError(f"{what}: {t} is not float32, bfloat16 or float16")
     return d
 
 
-def _rows(t, heads: int, what: str) -> int:
-    """The row stride, in elements, of a [rows, heads, 256] tensor whose heads lie side by side in a row."""
+def _rows(t, heads: int, what: str):
+    """(rows, row stride in elements) of a [rows, heads, 256] tensor whose heads lie side by side in a row."""
     sh, st = t.shape, t.stride()
-    if len(sh) != 3 or sh[1] != heads or sh[2] != HEAD_DIM or st[2] != 1 or (heads > 1 and st[1] != HEAD_DIM):
+    if len(sh) != 3 or sh[1] != heads or sh[2] != HEAD_DIM or st[2] != 1 or (st[1] != HEAD_DIM and heads > 1):
         raise KVQError(f"{what}: want [rows, {heads}, {HEAD_DIM}] with contiguous rows, got {tuple(sh)} with strides {st}")
-    return st[0] if sh[0] > 1 else heads * HEAD_DIM + (-heads * HEAD_DIM % 8)
+    n = sh[0]
+    return n, (st[0] if n > 1 else heads * HEAD_DIM)
 
 
 def _index(t, what: str) -> int:
     """Address of a contiguous int32 tensor."""
-    torch = _torch()
-    if t.dtype is not torch.int32 or not t.is_contiguous():
+    if t.dtype is not _torch().int32 or not t.is_contiguous():
         raise KVQError(f"{what} is not a contiguous int32 tensor")
     return t.data_ptr()
 
@@ -387,22 +393,31 @@ def kv_append_rope(pool: KVPool, layer: int, k, v, row_start, pos0, page_table, 
     first = k if k is not None else q
     if first is None or (k is None) != (v is None):
         raise KVQError("kv_append_rope failed: KVQ_EINVAL (k and v, q, or all three)")
-    n_rows, el = first.shape[0], first.dtype
-    dt = _dtype(el, "kv_append_rope")
+    el = first.dtype
+    dt = _dtypes.get(el)
+    if dt is None:
+        dt = _dtype(el, "kv_append_rope")
     kp = vp = qp = op = cp_ = None
     ks = vs = qs = n_pos = rot = odt = 0
+    n_rows = n_v = n_q = -1
     if k is not None:
-        ks, vs, kp, vp = _rows(k, d.n_kv_heads, "k"), _rows(v, d.n_kv_heads, "v"), k.data_ptr(), v.data_ptr()
-        if v.dtype is not el or v.shape[0] != n_rows:
+        heads = d.n_kv_heads
+        n_rows, ks = _rows(k, heads, "k")
+        n_v, vs = _rows(v, heads, "v")
+        kp, vp = k.data_ptr(), v.data_ptr()
+        if n_v != n_rows or v.dtype is not el:
             raise KVQError("kv_append_rope: v differs from k in type or rows")
     if q is not None:
-        qs, qp = _rows(q, d.n_q_heads, "q"), q.data_ptr()
-        if q.dtype is not el or q.shape[0] != n_rows:
+        n_q, qs = _rows(q, d.n_q_heads, "q")
+        qp = q.data_ptr()
+        if n_rows < 0:
+            n_rows = n_q
+        if n_q != n_rows or q.dtype is not el:
             raise KVQError("kv_append_rope: q differs from k in type or rows")
         if q_out is None:
             if q_out_dtype is None:
-                q_out_dtype = el if pool.fmt == FP8B else torch.float32
-            q_out = torch.empty((n_rows, d.n_q_heads, HEAD_DIM), dtype=q_out_dtype, device=q.device)
+                q_out_dtype = el if d.fmt == FP8B else torch.float32
+            q_out = q.new_empty((n_rows, d.n_q_heads, HEAD_DIM), dtype=q_out_dtype)
         elif q_out.shape != q.shape or not q_out.is_contiguous():
             raise KVQError("kv_append_rope: q_out is contiguous and shaped as q")
         odt, op = _dtype(q_out.dtype, "kv_append_rope"), q_out.data_ptr()
@@ -418,10 +433,11 @@ def kv_append_rope(pool: KVPool, layer: int, k, v, row_start, pos0, page_table, 
             raise KVQError("kv_append_rope: cos_sin is not a contiguous float32 tensor")
         cp_ = cos_sin.data_ptr()
     _on_current_device("kv_append_rope", pool.buf, first, v, q, q_out, row_start, pos0, page_table, cos_sin, status)
-    cp = pool.c_pool()
-    _check(lib().kv_append_rope(ctypes.byref(cp), layer, cp_, n_pos, rot, 1 if interleaved else 0, qp, kp, vp, dt, qs, ks, vs,
-                                n_rows, rs, p0, pt, max_pages, n_seq, op, odt, _ptr(status), _stream(stream)),
-           "kv_append_rope")
+    rc = lib().kv_append_rope(ctypes.byref(pool.c_pool()), layer, cp_, n_pos, rot, 1 if interleaved else 0, qp, kp, vp, dt, qs,
+                              ks, vs, n_rows, rs, p0, pt, max_pages, n_seq, op, odt, None if status is None else status.data_ptr(),
+                              _stream(stream))
+    if rc != 0:
+        _check(rc, "kv_append_rope")
     return q_out
 
 
@@ -448,8 +464,8 @@ def paged_prefill_attn_fp8b(pool: KVPool, layer: int, q, page_table, plan_dev, i
     strided), rotated as the keys are; plan_dev a device copy of prefill_plan's
     array; workspace None when info.workspace_bytes is 0."""
     what = "paged_prefill_attn_fp8b"
-    qs = _rows(q, pool.desc.n_q_heads, "q")
-    if q.shape[0] < info.n_rows:
+    n_rows, qs = _rows(q, pool.desc.n_q_heads, "q")
+    if n_rows < info.n_rows:
         raise KVQError(f"{what}: q has fewer rows than the plan")
     import torch
     for t, el in ((out_bf16, torch.bfloat16), (out_f32, torch.float32)):

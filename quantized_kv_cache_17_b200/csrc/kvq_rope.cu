@@ -314,6 +314,25 @@ struct Turn {
     }
 };
 
+// row_start and pos0 of a batch of fewer than 32 sequences, an entry a lane: one
+// load where a search and what it finds are two or three.
+struct Batch {
+    int start, pos0, n_seq;
+    __device__ __forceinline__ Batch(const RopeArgs &R, bool few, int lane) : start(0), pos0(0), n_seq(R.n_seq) {
+        if (few && lane <= R.n_seq) start = __ldg(R.row_start + lane);
+        if (few && lane < R.n_seq) pos0 = __ldg(R.pos0 + lane);
+    }
+    // the last sequence that starts at or below row, -1 if none (by the whole warp)
+    __device__ __forceinline__ int last_below(int row) const {
+        return 31 - __clz(__ballot_sync(0xffffffffu, (int)(threadIdx.x & 31) < n_seq && start <= row));
+    }
+    // the last sequence whose tile items start at or below item
+    __device__ __forceinline__ int last_tiles_below(int item) const {
+        const int lane = threadIdx.x & 31;
+        return 31 - __clz(__ballot_sync(0xffffffffu, lane < n_seq && (start >> 6) + 2 * lane <= item));
+    }
+};
+
 // Query rows: a warp takes n <= BA_ROWS consecutive (row, head) items, mostly of
 // one or two rows, whose angles it loads once.
 template <typename T, typename TQ> __device__ __forceinline__ void rope_queries(const RopeArgs &R, uint32_t item0, int n, int lane) {
@@ -412,13 +431,18 @@ __global__ void __launch_bounds__(BA_THREADS, 2) block_append_kernel(uint8_t *po
     }
     const bool is_v = blockIdx.x & 1;
     const int item = (blockIdx.x >> 1) / (unsigned)geo.n_kv_heads, head = (int)(blockIdx.x >> 1) - item * geo.n_kv_heads;
-    const int seq = by_row ? warp_find_last(R.n_seq, item, lane, [&](int s) { return (int64_t)__ldg(R.row_start + s); })
-                           : warp_find_last(R.n_seq, item, lane, [&](int s) { return (int64_t)(__ldg(R.row_start + s) >> 6) + 2 * (int64_t)s; });
+    const bool few = R.n_seq < 32;
+    const Batch all(R, few, lane);
+    const int seq = few      ? (by_row ? all.last_below(item) : all.last_tiles_below(item))
+                    : by_row ? warp_find_last(R.n_seq, item, lane, [&](int s) { return (int64_t)__ldg(R.row_start + s); })
+                             : warp_find_last(R.n_seq, item, lane, [&](int s) { return (int64_t)(__ldg(R.row_start + s) >> 6) + 2 * (int64_t)s; });
     if (seq < 0) {
         if (threadIdx.x == 0) status_or(R.status, KVQ_STATUS_BAD_PLAN);
         return;
     }
-    const int row0 = __ldg(R.row_start + seq), row1 = __ldg(R.row_start + seq + 1), p0 = __ldg(R.pos0 + seq);
+    const int row0 = few ? __shfl_sync(0xffffffffu, all.start, seq) : __ldg(R.row_start + seq);
+    const int row1 = few ? __shfl_sync(0xffffffffu, all.start, seq + 1) : __ldg(R.row_start + seq + 1);
+    const int p0 = few ? __shfl_sync(0xffffffffu, all.pos0, seq) : __ldg(R.pos0 + seq);
     if (row0 < 0 || row1 < row0 || row1 > R.n_rows) {
         if (threadIdx.x == 0) status_or(R.status, KVQ_STATUS_BAD_PLAN);
         return;
@@ -443,13 +467,18 @@ __global__ void __launch_bounds__(BA_THREADS, 2) block_append_kernel(uint8_t *po
     const int tok0 = BA_ROWS * warp;
     const Dims m(is_v ? 0 : R.rot_dim, R.interleaved, lane);
     Raw<T> raw[BA_ROWS];
+    Turn turn[BA_ROWS];
     float x[BA_ROWS][8];
+    const bool turned = !is_v && R.rot_dim;
     {
         const T *src = is_v ? static_cast<const T *>(R.v) : static_cast<const T *>(R.k);
         const int64_t stride = is_v ? R.v_stride : R.k_stride;
 #pragma unroll
         for (int i = 0; i < BA_ROWS; ++i)
-            if (tok0 + i >= t0 && tok0 + i < t1) raw[i].load(src + (rbase + tok0 + i) * stride + head * D, m);
+            if (tok0 + i >= t0 && tok0 + i < t1) {       // the angles with the values: asked for one by one they cost a wait each
+                raw[i].load(src + (rbase + tok0 + i) * stride + head * D, m);
+                if (turned) turn[i].load(R, (int)first + tok0 + i, lane, m);
+            }
     }
     if (slot < 0 || slot >= geo.n_pages) {
         if (threadIdx.x == 0) status_or(R.status, KVQ_STATUS_BAD_SLOT);
@@ -466,11 +495,7 @@ __global__ void __launch_bounds__(BA_THREADS, 2) block_append_kernel(uint8_t *po
     for (int i = 0; i < BA_ROWS; ++i) {
         if (tok0 + i >= t0 && tok0 + i < t1) {
             raw[i].get(x[i]);
-            if (!is_v && R.rot_dim) {
-                Turn turn;
-                turn.load(R, (int)first + tok0 + i, lane, m);
-                turn.apply(x[i], m);
-            }
+            if (turned) turn[i].apply(x[i], m);
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
                 asm("max.f32 %0, %1, %2, %3;" : "=f"(amax) : "f"(amax), "f"(fabsf(x[i][e])), "f"(fabsf(x[i][e + 1])));
@@ -499,8 +524,9 @@ __global__ void __launch_bounds__(BA_THREADS, 2) block_append_kernel(uint8_t *po
     for (int w = 0; w < BA_WARPS; ++w) amax = fmaxf(amax, s_max[w]);
     const float d = fmaxf(d0, block_scale(amax));
     if (threadIdx.x == 0) *scale = d;
-    const float f = d > 0.0f ? d0 / d : 1.0f;           // exact: both are powers of two (or d0 = 0)
-    const float inv = d > 0.0f ? 1.0f / d : 0.0f;        // x * inv is x / d
+    // 1 / d of a power of two with exponent within -120 .. 118: x * inv is x / d, and d0 / d is exact too
+    const float inv = d > 0.0f ? __uint_as_float((254u << 23) - __float_as_uint(d)) : 0.0f;
+    const float f = d > 0.0f ? d0 * inv : 1.0f;
     const bool grown = t0 > 0 && f != 1.0f;
     const bool staged = is_v && (grown || t1 - t0 > BA_DIRECT);
     if (!is_v) {
