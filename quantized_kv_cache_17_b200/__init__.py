@@ -234,8 +234,15 @@ def decode_plan(desc: PoolDesc, seq_lens: Sequence[int], max_pages: int, n_ctas:
     """Host split plan: returns (plan int32 numpy array, PlanInfo)."""
     sl = np.ascontiguousarray(np.asarray(seq_lens, np.int32))
     info = PlanInfo()
-    rc = lib().kvq_decode_plan(ctypes.byref(desc), len(sl), sl.ctypes.data, max_pages, n_ctas, None, 0,
-                               ctypes.byref(info))
+    if desc.fmt == FP8B:                             # its plan is searched for: once, with room for 160 CTAs' cuts
+        plan = np.empty(8 + 5 * (len(sl) * max(desc.n_kv_heads, 0) + 160) + 162, np.int32)
+        rc = lib().kvq_decode_plan(ctypes.byref(desc), len(sl), sl.ctypes.data, max_pages, n_ctas, plan.ctypes.data,
+                                   len(plan), ctypes.byref(info))
+        if rc == 0:
+            return plan[:info.plan_len].copy(), info
+    else:
+        rc = lib().kvq_decode_plan(ctypes.byref(desc), len(sl), sl.ctypes.data, max_pages, n_ctas, None, 0,
+                                   ctypes.byref(info))
     if rc != -5:
         _check(rc, "kvq_decode_plan")
     plan = np.zeros(info.plan_len, np.int32)
@@ -449,12 +456,15 @@ def prefill_plan(desc: PoolDesc, pos0: Sequence[int], n_tok: Sequence[int], max_
         raise KVQError("prefill_plan: pos0 and n_tok are lists of the same length")
     info = PrefillInfo()
     args = (ctypes.byref(desc), len(p), p.ctypes.data, n.ctypes.data, max_pages, n_ctas)
-    rc = lib().kvq_prefill_plan(*args, None, 0, ctypes.byref(info))
-    if rc != -5:
-        _check(rc, "kvq_prefill_plan")
-    plan = np.zeros(info.plan_len, np.int32)
-    _check(lib().kvq_prefill_plan(*args, plan.ctypes.data, len(plan), ctypes.byref(info)), "kvq_prefill_plan")
-    return plan, info
+    # room for every row tile and 160 CTAs' cuts at once, so that the plan is worked out once; more if that is too little
+    tiles = int((-(-np.maximum(n, 0).astype(np.int64) * (desc.n_q_heads // max(desc.n_kv_heads, 1)) // 128)).sum()) * desc.n_kv_heads
+    plan = np.empty(8 + 12 * (tiles + 160) + 9 * 160 + 1 if tiles < 1 << 24 else 0, np.int32)
+    rc = lib().kvq_prefill_plan(*args, plan.ctypes.data, len(plan), ctypes.byref(info))
+    if rc == -5:
+        plan = np.empty(info.plan_len, np.int32)
+        rc = lib().kvq_prefill_plan(*args, plan.ctypes.data, len(plan), ctypes.byref(info))
+    _check(rc, "kvq_prefill_plan")
+    return plan[:info.plan_len].copy(), info
 
 
 def paged_prefill_attn_fp8b(pool: KVPool, layer: int, q, page_table, plan_dev, info: PrefillInfo, workspace, out_bf16,
