@@ -117,6 +117,12 @@ static_assert(PfCfg<2>::SMEM <= 232448 && PfCfg<3>::SMEM <= 232448, "227 KB a CT
 
 __device__ __forceinline__ float pow2f(int e) { return e < -126 ? 0.0f : __uint_as_float((uint32_t)(min(e, 127) + 127) << 23); }
 
+__device__ __forceinline__ uint32_t h2_to_e4m3x2(uint32_t h) {       // nearest even, saturating
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+    return r;
+}
+
 // The whole pair of warps (64 threads, barrier id) agrees on whether any thread asks.
 __device__ __forceinline__ bool pair_any(bool ask, int id) {
     uint32_t r;
@@ -147,7 +153,18 @@ template <typename T> struct QueryRows {
             raw[y] = at < 0 ? make_uint4(0, 0, 0, 0) : __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(A.q) + at) + lane);
         }
     }
-    __device__ __forceinline__ void get(const PfbArgs &, const Unit &, int, int, int y, float (&x)[8]) const {
+    __device__ __forceinline__ float largest(const PfbArgs &, int, int y) const {
+        const uint32_t a = raw[y].x & 0x7FFF7FFFu, b = raw[y].y & 0x7FFF7FFFu, c = raw[y].z & 0x7FFF7FFFu, d = raw[y].w & 0x7FFF7FFFu;
+        if constexpr (std::is_same_v<T, __half>) {
+            const float2 f = __half22float2(__hmax2(__hmax2(u32_as_h2(a), u32_as_h2(b)), __hmax2(u32_as_h2(c), u32_as_h2(d))));
+            return fmaxf(f.x, f.y);
+        } else {
+            auto bf = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162 *>(&u); };
+            const __nv_bfloat162 m = __hmax2(__hmax2(bf(a), bf(b)), __hmax2(bf(c), bf(d)));
+            return fmaxf(__low2float(m), __high2float(m));
+        }
+    }
+    __device__ __forceinline__ void get(const PfbArgs &, int, int y, float (&x)[8]) const {
         const uint32_t w[4] = {raw[y].x, raw[y].y, raw[y].z, raw[y].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -166,7 +183,14 @@ template <> struct QueryRows<float> {
     static constexpr bool AHEAD = false;
     int64_t mine;
     __device__ __forceinline__ void load(const PfbArgs &A, const Unit &u, int warp, int lane) { mine = query_row(A, u, u.r0 + 16 * warp + (lane & 15)); }
-    __device__ __forceinline__ void get(const PfbArgs &A, const Unit &, int, int lane, int y, float (&x)[8]) const {
+    __device__ __forceinline__ float largest(const PfbArgs &A, int lane, int y) const {
+        float x[8], m = 0.0f;
+        get(A, lane, y, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
+        return m;
+    }
+    __device__ __forceinline__ void get(const PfbArgs &A, int lane, int y, float (&x)[8]) const {
         const int64_t at = __shfl_sync(0xffffffffu, mine, y);
         const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(A.q) + at) + 2 * lane;
         const float4 a = at < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldg(p), b = at < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : __ldg(p + 1);
@@ -421,33 +445,31 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
             const int n_rows = u.n_tok * A.G, nt = (u.k1 - u.k0 + PFB_KEYS - 1) / PFB_KEYS, kv_end = u.pos0 + u.n_tok;
             // ---- query terms: rows 16 warp .. + 15, eight dims a lane ----
             if (i == i0 || !QueryRows<T>::AHEAD) rows.load(A, u, warp, lane);
+            float top[16];                               // the rows' largest magnitudes, all reductions under way at once
+#pragma unroll
+            for (int y = 0; y < 16; ++y)                 // not negative: the bits order as the values
+                top[y] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(rows.largest(A, lane, y))));
 #pragma unroll
             for (int y = 0; y < 16; ++y) {
                 const int r = 16 * warp + y;
-                float x[8];
-                rows.get(A, u, warp, lane, y, x);
-                float mx = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
-                mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));   // not negative: the bits order as the values
-                const int kq = mx > 0.0f ? max(-114, min(114, 7 - ((int)(__float_as_uint(mx) >> 23) - 127))) : 0;
+                const int kq = top[y] > 0.0f ? max(-114, min(114, 7 - ((int)(__float_as_uint(top[y]) >> 23) - 127))) : 0;
                 const float up = pow2f(kq);
                 if (lane == 0) X.qscale[r] = pow2f(-kq) * (1.4426950408889634f / 16.0f);
+                // scaled as fp16: exact for 16-bit types down to what E4M3 terms reach, the 11 bits of three terms for fp32
+                float x[8];
+                rows.get(A, lane, y, x);
+                uint32_t h[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) h[e] = h2_as_u32(__floats2half2_rn(x[2 * e] * up, x[2 * e + 1] * up));
                 // dims 8 lane ..: half lane / 16, chunk (lane / 2) % 8, its low or high 8 bytes
                 uint8_t *dst = sm + (lane >> 4) * 16384 + (r >> 3) * 1024 + (r & 7) * 128 + ((((lane >> 1) & 7) ^ (r & 7)) << 4) + (lane & 1) * 8;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] *= up;
 #pragma unroll
                 for (int t = 0; t < TERMS; ++t) {
                     uint32_t w[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        w[e] = f32x2_to_e4m3x2(x[2 * e], x[2 * e + 1]);
-                        if (t + 1 < TERMS) {
-                            const float2 f = __half22float2(u32_as_h2(e4m3x2_to_h2(w[e])));
-                            x[2 * e] -= f.x;
-                            x[2 * e + 1] -= f.y;
-                        }
+                        w[e] = h2_to_e4m3x2(h[e]);
+                        if (t + 1 < TERMS) h[e] = h2_as_u32(__hsub2(u32_as_h2(h[e]), u32_as_h2(e4m3x2_to_h2(w[e]))));   // exact
                     }
                     *reinterpret_cast<uint2 *>(dst + t * 32768) = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
                 }
