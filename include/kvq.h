@@ -494,7 +494,11 @@ int kvq_prefill_plan(const kvq_pool_desc *desc, int n_seq, const int32_t *pos0, 
  *            at element r * q_stride, the sequences' rows one after another in
  *            the plan's order.  Scores are q.k_hat/16.  Q enters the tensor cores
  *            as a sum of E4M3 terms under one power of two per row: two terms for
- *            bf16, which hold its 8 bits, three (12 bits) for fp16 and fp32
+ *            bf16, which hold its 8 bits, three for fp16, which hold its 11, and
+ *            for fp32, rounded to 11 bits.  A NaN or an infinity in a row of q
+ *            makes that (token, head) NaN and no other.  Scores are fp32; beyond
+ *            2^20 in magnitude, where fp32 no longer resolves them, a row's
+ *            result may be NaN
  *  plan      device copy of the kvq_prefill_plan array; info its host info
  *  workspace device, at least info->workspace_bytes (may be NULL when that is 0),
  *            needs no initialisation; calls that share it must not overlap

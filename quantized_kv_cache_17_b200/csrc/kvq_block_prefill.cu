@@ -65,7 +65,8 @@ __device__ __forceinline__ bool plan_ok(const PfbArgs &A) {
 //   S[128 rows][128 keys] = sum over terms of Q_i K^T: a row of Q, scaled so that
 //     its largest value lies in [2^7, 2^8), is a sum of E4M3 terms, each the
 //     rounding of what the earlier ones leave.  Two terms hold bf16's 8 bits (4
-//     each) down to 2^-10, which is 2^-17 of the row's largest; three hold 12.
+//     each) down to 2^-10, which is 2^-17 of the row's largest; three hold fp16's 11,
+//     and fp32 is rounded to those.
 //   O[128 rows][256 dims] += sum over three terms of W_i V: a weight as fp16 (11
 //     bits), then three E5M2 terms of 3 bits each: E5M2 is the upper byte of fp16,
 //     so a term is an integer rounding of the bits and what it leaves an exact fp16
@@ -452,8 +453,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
 #pragma unroll
             for (int y = 0; y < 16; ++y) {
                 const int r = 16 * warp + y;
-                const int kq = top[y] > 0.0f ? max(-114, min(114, 7 - ((int)(__float_as_uint(top[y]) >> 23) - 127))) : 0;
-                const float up = pow2f(kq);
+                const int kq = top[y] > 0.0f ? min(114, 7 - ((int)(__float_as_uint(top[y]) >> 23) - 127)) : 0;
+                const float up = top[y] <= FLT_MAX ? pow2f(kq) : __uint_as_float(0x7FC00000u);     // an infinity makes its row NaN
                 if (lane == 0) X.qscale[r] = pow2f(-kq) * (1.4426950408889634f / 16.0f);
                 // scaled as fp16: exact for 16-bit types down to what E4M3 terms reach, the 11 bits of three terms for fp32
                 float x[8];

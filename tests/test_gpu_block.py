@@ -526,6 +526,28 @@ def test_prefill_values(case, dtype):
     check_prefill(cache, table, pos0, toks, q, out, of, DT[dtype])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("e", [-90, 115, 125])
+def test_queries_near_the_ends_of_the_range(dtype, e):
+    """q of 2^e or so against keys that bring the scores back to ordinary sizes."""
+    rng = np.random.default_rng(85)
+    pos0, toks = [200, 0], [30, 70]
+    lens = [p + t for p, t in zip(pos0, toks)]
+    table, n_slots = page_table(rng, lens)
+    cache = random_cache(rng, n_slots, 1)
+    cache.codes[:, :, 0] &= 0x9F                  # |k| below 2^-3 under a scale of 1
+    cache.scales[..., 0] = 2.0 ** -min(e, 120)
+    q = np.clip(rng.standard_normal((sum(toks), 4, 256)), -3.9, 3.9)
+    q = dev((q * 2.0 ** e / (32 if e > 120 else 1)).astype(np.float32), DT[dtype])
+    if e > 120:
+        q[:, :, 5] = 1.5 * 2.0 ** e
+    out, of = prefill(make_pool(cache, 4), q, dev(table), pos0, toks)
+    check_prefill(cache, table, pos0, toks, q, out, of, DT[dtype])
+    last = torch.stack([q[29], q[99]]).float()
+    out, of = decode(make_pool(cache, 4), last, dev(table), lens)
+    check_decode(cache, table, lens, last.cpu().numpy(), out, of)
+
+
 def test_prefill_bad_slots_and_plans():
     rng = np.random.default_rng(90)
     lens, pos0, toks = [900], [890], [10]
