@@ -136,15 +136,14 @@ __device__ __forceinline__ bool pair_any(bool ask, int id) {
 }
 
 // The 16 query rows of a warp (rows 16 warp .. of the tile, zeros past the last), eight dims a lane.  16-bit rows are
-// held as they are, all 16 loaded at once and a unit ahead of their use; fp32 rows would need twice the registers and
-// are read when they are used.
+// held as they are, all 16 loaded at once (kept from before the unit before's result was written they were spilled, one
+// wait each: 8,000 cycles a unit against 1,000); fp32 rows would need twice the registers and are read when they are used.
 __device__ __forceinline__ int64_t query_row(const PfbArgs &A, const Unit &u, int r) {
     if (r >= u.n_tok * A.G) return -1;
     const int tok = r / A.G;
     return (int64_t)(u.row_start + tok) * A.q_stride + (u.head * A.G + r - tok * A.G) * D;
 }
 template <typename T> struct QueryRows {
-    static constexpr bool AHEAD = true;
     uint4 raw[16];
     __device__ __forceinline__ void load(const PfbArgs &A, const Unit &u, int warp, int lane) {
         const int64_t mine = query_row(A, u, u.r0 + 16 * warp + (lane & 15));
@@ -181,7 +180,6 @@ template <typename T> struct QueryRows {
     }
 };
 template <> struct QueryRows<float> {
-    static constexpr bool AHEAD = false;
     int64_t mine;
     __device__ __forceinline__ void load(const PfbArgs &A, const Unit &u, int warp, int lane) { mine = query_row(A, u, u.r0 + 16 * warp + (lane & 15)); }
     __device__ __forceinline__ float largest(const PfbArgs &A, int lane, int y) const {
@@ -245,7 +243,7 @@ __device__ __forceinline__ void split_weights(uint32_t a, uint32_t b, uint32_t &
     t2 = __byte_perm(a2, b2, 0x7531);
     const uint32_t sa = h2_as_u32(__hsub2(u32_as_h2(ra), u32_as_h2(a2 & 0xFF00FF00u)));
     const uint32_t sb = h2_as_u32(__hsub2(u32_as_h2(rb), u32_as_h2(b2 & 0xFF00FF00u)));
-    t3 = __byte_perm(sa + 0x00800080u, sb + 0x00800080u, 0x7531);
+    t3 = __byte_perm(sa, sb, 0x7531);                // what is left of 11 bits has 3 at most: nothing to round above 2^-6
 }
 
 template <typename T, int TERMS>
@@ -426,7 +424,6 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(PF_REGS_SOFT));
         const int part = warp >> 2, row = 32 * (warp & 3) + lane, bar = 1 + (warp & 3);
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        QueryRows<T> rows;
         int it = 0;
         auto wait_s = [&](uint64_t *bar, uint32_t parity) {     // as wait, without its answer
             if (!mbar_try_wait(bar, parity)) {
@@ -445,7 +442,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
             if (!load_unit(A, i, u)) continue;
             const int n_rows = u.n_tok * A.G, nt = (u.k1 - u.k0 + PFB_KEYS - 1) / PFB_KEYS, kv_end = u.pos0 + u.n_tok;
             // ---- query terms: rows 16 warp .. + 15, eight dims a lane ----
-            if (i == i0 || !QueryRows<T>::AHEAD) rows.load(A, u, warp, lane);
+            QueryRows<T> rows;
+            rows.load(A, u, warp, lane);
             float top[16];                               // the rows' largest magnitudes, all reductions under way at once
 #pragma unroll
             for (int y = 0; y < 16; ++y)                 // not negative: the bits order as the values
@@ -479,6 +477,15 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
             __syncwarp();
             if (lane == 0) mbar_arrive(&X.q_full);
             asm volatile("bar.sync 5, %0;" ::"n"(PF_SOFT * 32) : "memory");      // qscale of every row
+            if (i + 1 < i1) {                            // the next unit's rows come to L2 meanwhile
+                Unit v;
+                if (load_unit(A, i + 1, v)) {
+                    const int64_t at = query_row(A, v, v.r0 + 16 * warp + (lane & 15));
+                    if (at >= 0)
+                        for (int x = lane >> 4; x < 2 * (int)sizeof(T); x += 2)
+                            asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint8_t *>(static_cast<const T *>(A.q) + at) + 128 * x));
+                }
+            }
             const float qs = X.qscale[row];
             const int r = u.r0 + row;
             const int limit = r < n_rows ? min(u.k1, u.pos0 + r / A.G + 1) : u.k1;
@@ -636,10 +643,6 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&X.p_full);
-            }
-            if (QueryRows<T>::AHEAD && i + 1 < i1) {
-                Unit v;
-                if (load_unit(A, i + 1, v)) rows.load(A, v, warp, lane);
             }
             // ---- the unit's result ----
             wait_s(&X.o_done, (it - 1) & 1);
