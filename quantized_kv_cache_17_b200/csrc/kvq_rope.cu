@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(128) rope_append_kernel(uint8_t *pool, PoolGeo
 // ---- fp8b ------------------------------------------------------------------
 constexpr int BA_WARPS = 16, BA_THREADS = BA_WARPS * 32;
 constexpr int BA_ROWS = 4;             // rows of a warp, all loaded before the first is used
+constexpr int BA_MANY = 8;             // query items of a warp where there are many (16-bit types: fp32 ones would be spilled)
 constexpr int64_t BA_FEW = 4736;       // (row, head) items that get a warp each: 148 SMs x 2 CTAs x 16 warps
 constexpr int BA_DIRECT = 4;           // tokens of a tile up to which their V codes are stored byte by byte
 static_assert(BA_WARPS * BA_ROWS == BT && BA_ROWS == 4, "a CTA holds a tile's rows, a warp the tokens of one word of V codes");
@@ -333,20 +334,20 @@ struct Batch {
     }
 };
 
-// Query rows: a warp takes n <= BA_ROWS consecutive (row, head) items, mostly of
-// one or two rows, whose angles it loads once.
-template <typename T, typename TQ> __device__ __forceinline__ void rope_queries(const RopeArgs &R, uint32_t item0, int n, int lane) {
+// Query rows: a warp takes n <= N consecutive (row, head) items, mostly of one or
+// two rows, whose angles it loads once.
+template <typename T, typename TQ, int N> __device__ __forceinline__ void rope_queries(const RopeArgs &R, uint32_t item0, int n, int lane) {
     const uint32_t n_items = (uint32_t)(R.n_rows * R.n_q_heads), n_q = (uint32_t)R.n_q_heads;   // at most 2^31
     if (item0 >= n_items) return;
     n = (int)min((uint32_t)n, n_items - item0);
     const uint32_t row0 = item0 / n_q, head0 = item0 - row0 * n_q;
     const Dims m(R.rot_dim, R.interleaved, lane);
-    Raw<T> raw[BA_ROWS];
+    Raw<T> raw[N];
     {
         uint32_t h = head0;
         const T *src = static_cast<const T *>(R.q) + (int64_t)row0 * R.q_stride;
 #pragma unroll
-        for (int y = 0; y < BA_ROWS; ++y) {
+        for (int y = 0; y < N; ++y) {
             if (y < n) raw[y].load(src + h * D, m);
             if (++h == n_q) h = 0, src += R.q_stride;
         }
@@ -374,7 +375,7 @@ template <typename T, typename TQ> __device__ __forceinline__ void rope_queries(
     int held = -1;
     TQ *dst = static_cast<TQ *>(R.q_out) + (int64_t)item0 * D;
 #pragma unroll
-    for (int y = 0; y < BA_ROWS; ++y) {
+    for (int y = 0; y < N; ++y) {
         const int p = __shfl_sync(0xffffffffu, pos, y);
         if (p < 0) continue;
         float x[8];
@@ -426,7 +427,9 @@ __global__ void __launch_bounds__(BA_THREADS, 2) block_append_kernel(uint8_t *po
     grid_dependency_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (blockIdx.x >= kv_blocks) {
-        rope_queries<T, TQ>(R, ((blockIdx.x - kv_blocks) * BA_WARPS + warp) * q_rows, q_rows, lane);
+        const uint32_t item0 = ((blockIdx.x - kv_blocks) * BA_WARPS + warp) * q_rows;
+        if (q_rows <= BA_ROWS) rope_queries<T, TQ, BA_ROWS>(R, item0, q_rows, lane);
+        else if constexpr (sizeof(T) == 2) rope_queries<T, TQ, BA_MANY>(R, item0, q_rows, lane);
         return;
     }
     const bool is_v = blockIdx.x & 1;
@@ -462,6 +465,7 @@ __global__ void __launch_bounds__(BA_THREADS, 2) block_append_kernel(uint8_t *po
     if (by_row && item > row0 && (int64_t)p0 + (item - row0) != first) return;   // not the tile's first row
     const int slot = __ldg(R.page_table + (int64_t)seq * R.max_pages + (first >> 8));
     const int t0 = first >= p0 ? 0 : (int)(p0 - first), t1 = (int)min((int64_t)BT, end - first);
+    if (t0 >= t1) return;                                // the sequence starts past its room
     // the rows; the tile's token 0 would be row rbase (it may lie before row0)
     const int64_t rbase = row0 + (first - p0);
     const int tok0 = BA_ROWS * warp;
@@ -470,15 +474,17 @@ __global__ void __launch_bounds__(BA_THREADS, 2) block_append_kernel(uint8_t *po
     Turn turn[BA_ROWS];
     float x[BA_ROWS][8];
     const bool turned = !is_v && R.rot_dim;
-    {
-        const T *src = is_v ? static_cast<const T *>(R.v) : static_cast<const T *>(R.k);
+    const bool any = tok0 < t1 && tok0 + BA_ROWS > t0;   // the warp has rows; a token of its four that is not the call's stands for
+                                                         // one that is, so that nothing below has to ask
+    if (any) {
+        const T *src = (is_v ? static_cast<const T *>(R.v) : static_cast<const T *>(R.k)) + head * D;
         const int64_t stride = is_v ? R.v_stride : R.k_stride;
 #pragma unroll
-        for (int i = 0; i < BA_ROWS; ++i)
-            if (tok0 + i >= t0 && tok0 + i < t1) {       // the angles with the values: asked for one by one they cost a wait each
-                raw[i].load(src + (rbase + tok0 + i) * stride + head * D, m);
-                if (turned) turn[i].load(R, (int)first + tok0 + i, lane, m);
-            }
+        for (int i = 0; i < BA_ROWS; ++i) {              // the angles with the values: asked for one by one they cost a wait each
+            const int tok = min(max(tok0 + i, t0), t1 - 1);
+            raw[i].load(src + (rbase + tok) * stride, m);
+            if (turned) turn[i].load(R, (int)first + tok, lane, m);
+        }
     }
     if (slot < 0 || slot >= geo.n_pages) {
         if (threadIdx.x == 0) status_or(R.status, KVQ_STATUS_BAD_SLOT);
@@ -491,9 +497,9 @@ __global__ void __launch_bounds__(BA_THREADS, 2) block_append_kernel(uint8_t *po
 
     float amax = 0.0f;
     uint64_t odd2 = 0;                                   // NaN once a value is not finite
+    if (any) {
 #pragma unroll
-    for (int i = 0; i < BA_ROWS; ++i) {
-        if (tok0 + i >= t0 && tok0 + i < t1) {
+        for (int i = 0; i < BA_ROWS; ++i) {
             raw[i].get(x[i]);
             if (turned) turn[i].apply(x[i], m);
 #pragma unroll
@@ -510,7 +516,6 @@ __global__ void __launch_bounds__(BA_THREADS, 2) block_append_kernel(uint8_t *po
         amax = 0.0f;
 #pragma unroll
         for (int i = 0; i < BA_ROWS; ++i)
-            if (tok0 + i >= t0 && tok0 + i < t1)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     if (!(fabsf(x[i][e]) <= FLT_MAX)) x[i][e] = x[i][e] != x[i][e] ? 0.0f : copysignf(FLT_MAX, x[i][e]);
@@ -594,9 +599,10 @@ cudaError_t launch_typed(int fmt, uint8_t *pool, const PoolGeom &geo, const Rope
         const int64_t by_tiles = (R.n_rows >> 6) + 2 * (int64_t)R.n_seq;
         const int by_row = R.n_rows < by_tiles ? 1 : 0;
         const int64_t kv = R.k ? (by_row ? R.n_rows : by_tiles) * geo.n_kv_heads * 2 : 0;
-        // a few query rows are spread over as many warps; many are taken BA_ROWS at a time, for the loads in flight and
-        // the angles they share
-        const int q_rows = q_items <= BA_FEW ? 1 : BA_ROWS;
+        // a few query rows are spread over as many warps; more are taken BA_ROWS at a time, for the loads in flight and
+        // the angles they share, and very many BA_MANY at a time, for the instructions around them (4 and 8 a warp, 24
+        // heads: 2,000 rows 15.6 and 15.7 us, 3,000 rows 22.2 and 21.7, 8,917 rows 60.7 and 55)
+        const int q_rows = q_items <= BA_FEW ? 1 : sizeof(T) == 2 && q_items > 12 * BA_FEW ? BA_MANY : BA_ROWS;
         const int64_t qb = (q_items + BA_WARPS * q_rows - 1) / (BA_WARPS * q_rows);
         return launch_ex(block_append_kernel<T, TQ>, dim3((unsigned)(kv + qb)), dim3(BA_THREADS), 0, s, false, pool, geo,
                          R, (unsigned)kv, by_row, q_rows);

@@ -192,6 +192,28 @@ def test_append_decoding_batch_with_padding():
     run_appends([[1] * 40, [2] * 40], 4, 1, torch.float16, 32, True, False, [3] * 40, 13, pad=2)
 
 
+@pytest.mark.parametrize("hq,hkv,toks,dtype,inter", [(24, 4, [0, 1701, 40, 0, 660], "bf16", False), (7, 1, [8200], "f16", True),
+                                                     (24, 3, [2400], "f32", False)])
+def test_append_of_many_query_rows(hq, hkv, toks, dtype, inter):
+    """As many query rows as make a warp take eight, of one row and of several, of sequences that end between them."""
+    run_appends([toks], hq, hkv, DT[dtype], 64, inter, False, [max(t, 1) for t in toks], 14, pad=5, stride_extra=1)
+
+
+def test_append_that_starts_past_the_rotation_table():
+    """The place lies in a tile that the table still reaches: nothing is read or written for it."""
+    rng = np.random.default_rng(15)
+    model = br.Cache(2, 1)
+    model.codes[:], model.scales[:] = rng.integers(0, 256, model.codes.shape, dtype=np.uint8), 1.0
+    pool, status = make_pool(model, 1), i32([0])
+    k, q = dev(rng.standard_normal((9, 1, 256)).astype(np.float32)), torch.zeros((9, 1, 256), device="cuda")
+    out = torch.full((9, 1, 256), 5.0, device="cuda")
+    kvq.kv_append_rope(pool, 0, k, k, i32([0, 9]), i32([25]), i32([[0, 1]]), cos_sin=dev(br.rope_table(22, 64)), q=q, q_out=out,
+                       status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == kvq.STATUS_BAD_SLOT and (out == 5).all()
+    assert np.array_equal(pool_bytes_of(pool), model.pack())
+
+
 def test_append_of_no_rows():
     pool = make_pool(br.Cache(2, 2), 4)
     before = pool.buf.clone()
