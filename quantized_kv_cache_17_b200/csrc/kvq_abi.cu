@@ -2,6 +2,9 @@
 // launches.  See include/kvq.h for the contract of every entry point.
 #include <algorithm>
 #include <cstring>
+#include <functional>
+#include <memory>
+#include <new>
 #include <vector>
 
 #include "kvq_block.cuh"
@@ -71,7 +74,7 @@ int check_pool(const kvq_pool *pool, int layer, PoolGeom *geo) {
 // prompt took 949, 811, 780 and 765 us planned with 3, 5, 7 and 9, 512 tokens at
 // 32,768 386, 384, 369 and 366), and the shortest part worth a partial result (8 x 5
 // tokens at 64 to 4,095 keys: 27.3, 28.7, 29.0, 31.8 and 34.4 us with 1, 2, 3, 4 and 6).
-constexpr int64_t PFB_TILE_COST = 8, PFB_MIN_PART = 2;
+constexpr int64_t PFB_TILE_COST = 8, PFB_MIN_PART = 2, PFB_CUT_COST = 4;
 
 // Decode plan of fp8b: what a unit costs beyond its steps of 64 tokens, in steps
 // (its query, the merge of its warps, its result and its share of the units' merge;
@@ -627,7 +630,49 @@ int kvq_prefill_plan(const kvq_pool_desc *desc, int n_seq, const int32_t *pos0, 
         if (walk(mid, nullptr, nullptr, nullptr).ctas <= n_ctas) hi = mid;
         else lo = mid + 1;
     }
-    const Count c = walk(lo, nullptr, nullptr, nullptr);
+    Count c = walk(lo, nullptr, nullptr, nullptr);
+    // Where whole tiles, the longest first, each to the CTA with the least, come out
+    // about as even, nothing is cut.  (Not tried for so many that cuts are a small
+    // share of the work.)
+    struct Tile {
+        int64_t steps, row_start;
+        int32_t b, g, r0, cta;
+    };
+    using Load = std::pair<int64_t, int32_t>;
+    const int32_t n_whole = (int32_t)std::min<int64_t>(n_ctas, tiles);
+    const bool try_whole = c.merges > 0 && tiles <= (1 << 18);
+    std::unique_ptr<Tile[]> whole(try_whole ? new (std::nothrow) Tile[tiles] : nullptr);
+    std::unique_ptr<Load[]> least(try_whole ? new (std::nothrow) Load[n_whole] : nullptr);
+    if (whole && least) {
+        int64_t row_start = 0, longest = 0, n = 0;
+        for (int b = 0; b < n_seq; row_start += n_tok[b], ++b)
+            for (int g = 0; g < n_kv; ++g)
+                for (int64_t r0 = 0; r0 < (int64_t)n_tok[b] * G; r0 += PFB_ROWS)
+                    whole[n++] = {steps_of(b, r0), row_start, b, g, (int32_t)r0, 0};
+        auto in_order = [](const Tile &x, const Tile &y) {
+            return x.b != y.b ? x.b < y.b : x.g != y.g ? x.g < y.g : x.r0 < y.r0;
+        };
+        std::sort(whole.get(), whole.get() + n, [&](const Tile &x, const Tile &y) { return x.steps != y.steps ? x.steps > y.steps : in_order(x, y); });
+        for (int32_t i = 0; i < n_whole; ++i) least[i] = {0, i};         // a heap already
+        for (int64_t i = 0; i < n && longest <= lo + PFB_CUT_COST; ++i) {
+            std::pop_heap(least.get(), least.get() + n_whole, std::greater<Load>());
+            Load &x = least[n_whole - 1];
+            whole[i].cta = x.second;
+            x.first += whole[i].steps + PFB_TILE_COST;
+            longest = std::max(longest, x.first);
+            std::push_heap(least.get(), least.get() + n_whole, std::greater<Load>());
+        }
+        if (longest <= lo + PFB_CUT_COST) {
+            c = Count{tiles, 0, 0, n_whole};
+            std::sort(whole.get(), whole.get() + n, [&](const Tile &x, const Tile &y) {
+                return x.cta != y.cta ? x.cta < y.cta : x.steps != y.steps ? x.steps > y.steps : in_order(x, y);
+            });
+        } else {
+            whole.reset();
+        }
+    } else {
+        whole.reset();
+    }
     const int64_t len = pfb_plan_len(c.units, c.merges, c.ctas);
     if (len > INT32_MAX) return KVQ_EUNSUPPORTED;
     info->n_units = (int32_t)c.units;
@@ -645,7 +690,19 @@ int kvq_prefill_plan(const kvq_pool_desc *desc, int n_seq, const int32_t *pos0, 
     const int32_t head[PLAN_HEADER] = {PFB_MAGIC, (int32_t)c.units, n_seq, (int32_t)rows, n_kv, G, (int32_t)c.merges, (int32_t)c.ctas};
     std::copy(head, head + PLAN_HEADER, plan);
     int32_t *U = plan + PLAN_HEADER, *M = U + c.units * PFB_UNIT;
-    walk(lo, U, M, M + c.merges * PFB_MERGE);
+    if (!whole) {
+        walk(lo, U, M, M + c.merges * PFB_MERGE);
+        return KVQ_OK;
+    }
+    int32_t *S = M;                        // no merges
+    S[0] = 0;
+    for (int64_t i = 0; i < tiles; ++i) {
+        const Tile &t = whole[i];
+        const int64_t keys = std::min<int64_t>(n_tok[t.b], ((int64_t)t.r0 + PFB_ROWS - 1) / G + 1) + pos0[t.b];
+        const int32_t u[PFB_UNIT] = {t.b, t.g, t.r0, 0, (int32_t)keys, -1, (int32_t)t.row_start, pos0[t.b], n_tok[t.b], 0, 0, 0};
+        std::copy(u, u + PFB_UNIT, U + i * PFB_UNIT);
+        S[t.cta + 1] = (int32_t)i + 1;
+    }
     return KVQ_OK;
 }
 
