@@ -70,11 +70,17 @@ int check_pool(const kvq_pool *pool, int layer, PoolGeom *geo) {
 }
 
 // Prefill plan: what a part of a row tile costs beyond its steps of 128 keys, in
-// steps (its query, its output and the rescaling of its first steps; a 7,777-token
-// prompt took 949, 811, 780 and 765 us planned with 3, 5, 7 and 9, 512 tokens at
-// 32,768 386, 384, 369 and 366), and the shortest part worth a partial result (8 x 5
-// tokens at 64 to 4,095 keys: 27.3, 28.7, 29.0, 31.8 and 34.4 us with 1, 2, 3, 4 and 6).
-constexpr int64_t PFB_TILE_COST = 8, PFB_MIN_PART = 2, PFB_CUT_COST = 4;
+// steps (its query, its output and the rescaling of its first steps; prompts of 568,
+// 873 and 170 tokens, the second at 5,604, took 156, 146, 142.5 and 146 us planned
+// with 4, 5, 6 and 8, 512 tokens at 32,768 340, 341.5, 340.5 and 339.5), the shortest
+// part worth a partial result (8 x 5 tokens at 64 to 4,095 keys: 27.3, 28.7, 29.0,
+// 31.8 and 34.4 us with 1, 2, 3, 4 and 6), and how much longer than the cut plan's
+// the longest CTA may be with whole tiles, which need no partial results and no merge:
+// with more tiles than CTAs, where cuts are units on top of the tiles (us cut and
+// whole: 4 steps longer 67.0 and 62.0, 8 longer 394 and 389, 10 longer 320 and 319.5,
+// 13 longer 369 and 372, 16 longer 154 and 173), and with fewer, where a part is all
+// that a CTA has (2 longer 18.2 and 18.4, 4 longer 18.0 and 21.2, 6 longer 18.3 and 23.9).
+constexpr int64_t PFB_TILE_COST = 8, PFB_MIN_PART = 2, PFB_CUT_COST = 10, PFB_CUT_COST_FEW = 2;
 
 // Decode plan of fp8b: what a unit costs beyond its steps of 64 tokens, in steps
 // (its query, the merge of its warps, its result and its share of the units' merge;
@@ -640,6 +646,7 @@ int kvq_prefill_plan(const kvq_pool_desc *desc, int n_seq, const int32_t *pos0, 
     };
     using Load = std::pair<int64_t, int32_t>;
     const int32_t n_whole = (int32_t)std::min<int64_t>(n_ctas, tiles);
+    const int64_t limit = lo + (tiles > n_ctas ? PFB_CUT_COST : PFB_CUT_COST_FEW);
     const bool try_whole = c.merges > 0 && tiles <= (1 << 18);
     std::unique_ptr<Tile[]> whole(try_whole ? new (std::nothrow) Tile[tiles] : nullptr);
     std::unique_ptr<Load[]> least(try_whole ? new (std::nothrow) Load[n_whole] : nullptr);
@@ -654,7 +661,7 @@ int kvq_prefill_plan(const kvq_pool_desc *desc, int n_seq, const int32_t *pos0, 
         };
         std::sort(whole.get(), whole.get() + n, [&](const Tile &x, const Tile &y) { return x.steps != y.steps ? x.steps > y.steps : in_order(x, y); });
         for (int32_t i = 0; i < n_whole; ++i) least[i] = {0, i};         // a heap already
-        for (int64_t i = 0; i < n && longest <= lo + PFB_CUT_COST; ++i) {
+        for (int64_t i = 0; i < n && longest <= limit; ++i) {
             std::pop_heap(least.get(), least.get() + n_whole, std::greater<Load>());
             Load &x = least[n_whole - 1];
             whole[i].cta = x.second;
@@ -662,7 +669,7 @@ int kvq_prefill_plan(const kvq_pool_desc *desc, int n_seq, const int32_t *pos0, 
             longest = std::max(longest, x.first);
             std::push_heap(least.get(), least.get() + n_whole, std::greater<Load>());
         }
-        if (longest <= lo + PFB_CUT_COST) {
+        if (longest <= limit) {
             c = Count{tiles, 0, 0, n_whole};
             std::sort(whole.get(), whole.get() + n, [&](const Tile &x, const Tile &y) {
                 return x.cta != y.cta ? x.cta < y.cta : x.steps != y.steps ? x.steps > y.steps : in_order(x, y);

@@ -93,6 +93,34 @@ def test_prefill_plan_is_even():
     assert info.n_ctas == 148 and per.max() <= 1.1 * per.mean()
 
 
+@pytest.mark.parametrize("pos0,toks,whole", [([0], [7777], True), ([0, 901], [1025, 2047], True), ([32256], [512], False),
+                                             ([5604, 0], [873, 568], False)])
+def test_prefill_plan_cuts_tiles_only_where_whole_ones_are_uneven(pos0, toks, whole):
+    d = kvq.make_desc(1, 4, 24, 8, "fp8b")
+    plan, info = kvq.prefill_plan(d, pos0, toks, max_pages=1024, n_ctas=148)
+    u, _, start = _units(plan, info)
+    tiles = 4 * sum(-(-6 * n // 128) for n in toks)
+    if whole:
+        per = np.add.reduceat((u[:, 4] - u[:, 3] + 127) // 128 + 8, start[:-1])
+        assert info.n_units == tiles and info.n_merges == info.n_slots == 0 and info.workspace_bytes == 0
+        assert info.n_ctas == min(148, tiles) and per.max() <= 1.1 * per.mean() + 10
+    else:
+        assert info.n_units > tiles and info.n_merges > 0
+
+
+def test_prefill_plan_does_not_depend_on_the_room_for_it():
+    d = kvq.make_desc(1, 2, 16, 8, "fp8b")
+    for pos0, toks in (([0, 0, 7], [900, 3, 400]), ([9000], [64])):
+        plan, info = kvq.prefill_plan(d, pos0, toks, max_pages=1024, n_ctas=148)
+        a, b = np.array(pos0, np.int32), np.array(toks, np.int32)
+        exact, again = np.empty(info.plan_len, np.int32), kvq.PrefillInfo()
+        args = (ctypes.byref(d), len(a), a.ctypes.data, b.ctypes.data, 1024, 148)
+        assert kvq.lib().kvq_prefill_plan(*args, exact.ctypes.data, info.plan_len - 1, ctypes.byref(again)) == -5
+        assert again.plan_len == info.plan_len
+        assert kvq.lib().kvq_prefill_plan(*args, exact.ctypes.data, info.plan_len, ctypes.byref(again)) == 0
+        assert np.array_equal(plan, exact) and bytes(info) == bytes(again)
+
+
 def _pool(fmt="fp8b", hq=24, hkv=4):
     return kvq.Pool(0x10000, kvq.make_desc(1, hkv, hq, 8, fmt))
 
