@@ -464,9 +464,9 @@ int paged_decode_attn_fp8b_combined(const kvq_pool *pool, int layer, const float
 /* Plan of a ragged prefill (host only): sequence s brings n_tok[s] >= 0 new
  * tokens at positions pos0[s] .., so its token i attends to the keys
  * 0 .. pos0[s] + i.  The (token, query head) rows of each KV head are taken in
- * tiles of 128, and the plan deals the tiles' key ranges, in steps of 128 keys, to
- * n_ctas CTAs (0 = one per SM of the current device) as evenly as possible; a tile
- * cut between CTAs is merged from partial results in the workspace.  pos0, n_tok:
+ * tiles of 128, and the plan deals the tiles, or their key ranges in steps of 128
+ * keys, to n_ctas CTAs (0 = one per SM of the current device) as evenly as possible;
+ * a tile cut between CTAs is merged from partial results in the workspace.  pos0, n_tok:
  * host int32 [n_seq], pos0[s] >= 0 and pos0[s] + n_tok[s] <= max_pages * 256.
  * plan, plan_capacity, info: as for kvq_decode_plan (KVQ_ESIZE with
  * info->plan_len set when the array is too small).  KVQ_EUNSUPPORTED for a
