@@ -192,11 +192,12 @@ def test_append_decoding_batch_with_padding():
     run_appends([[1] * 40, [2] * 40], 4, 1, torch.float16, 32, True, False, [3] * 40, 13, pad=2)
 
 
-@pytest.mark.parametrize("hq,hkv,toks,dtype,inter", [(24, 4, [0, 1701, 40, 0, 660], "bf16", False), (7, 1, [8200], "f16", True),
-                                                     (24, 3, [2400], "f32", False)])
-def test_append_of_many_query_rows(hq, hkv, toks, dtype, inter):
+@pytest.mark.parametrize("hq,hkv,toks,dtype,inter,q_f32", [
+    (24, 4, [0, 1701, 40, 0, 660], "bf16", False, False), (7, 1, [8200], "f16", True, False), (24, 3, [2400], "f32", False, False),
+    (16, 2, [3600], "bf16", True, True), (1, 1, [57000, 3], "f16", False, False), (8, 1, [200] * 36, "bf16", False, True)])
+def test_append_of_many_query_rows(hq, hkv, toks, dtype, inter, q_f32):
     """As many query rows as make a warp take eight, of one row and of several, of sequences that end between them."""
-    run_appends([toks], hq, hkv, DT[dtype], 64, inter, False, [max(t, 1) for t in toks], 14, pad=5, stride_extra=1)
+    run_appends([toks], hq, hkv, DT[dtype], 64, inter, q_f32, [max(t, 1) for t in toks], 14, pad=5, stride_extra=1)
 
 
 def test_append_that_starts_past_the_rotation_table():
@@ -509,6 +510,23 @@ def test_prefill_splits(n_ctas, pos0, toks):
     check_prefill(cache, table, pos0, toks, q, out, of, torch.bfloat16)
     out2, of2 = prefill(pool, q, dev(table), pos0, toks, n_ctas=n_ctas)
     assert torch.equal(of, of2)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_prefill_of_whole_tiles(dtype):
+    """More row tiles than CTAs and none of them cut: the plan deals them out of order, several to a CTA."""
+    rng = np.random.default_rng(75)
+    pos0, toks = [0, 333, 5], [1300, 400, 1]
+    lens = [p + t for p, t in zip(pos0, toks)]
+    table, n_slots = page_table(rng, lens)
+    cache = random_cache(rng, n_slots, 2)
+    spoil_after(cache, table, lens)
+    q = rows_of(rng.standard_normal((sum(toks) + 3, 16, 256)).astype(np.float32), None, DT[dtype], stride_extra=2)
+    pool = make_pool(cache, 16)
+    _, info = kvq.prefill_plan(pool.desc, pos0, toks, table.shape[1], 148)
+    assert info.n_units > 148 and info.n_merges == 0
+    out, of = prefill(pool, q, dev(table), pos0, toks, n_ctas=148)
+    check_prefill(cache, table, pos0, toks, q, out, of, DT[dtype])
 
 
 @pytest.mark.parametrize("case", ["wide_scales", "zero_blocks", "one_key", "large_q", "zero_q", "tiny_v", "growing", "sink"])
