@@ -422,7 +422,6 @@ template <int SPLIT> __global__ void __launch_bounds__(BM_THREADS) block_merge_k
     const int64_t stride = ws_unit_floats(G);
     const float *ws = A.ws + u0 * stride, *mine = ws + min(h, G - 1) * D + (blockIdx.x % SPLIT) * (D / SPLIT) + 4 * c;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (tid < 8) s_M[tid] = -INFINITY, s_L[tid] = 0.0f;
     for (int c0 = 0; c0 < n; c0 += CHUNK) {        // 128 units at a time
         const int nc = min(CHUNK, n - c0);
         float4 v[BM_BATCH];
@@ -431,7 +430,9 @@ template <int SPLIT> __global__ void __launch_bounds__(BM_THREADS) block_merge_k
             const int x = pt + PARTS * b;
             v[b] = x < nc ? *reinterpret_cast<const float4 *>(mine + (c0 + x) * stride) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        if (warp < G) {                            // head `warp`: the reference, the units' factors, the sum
+        // head `warp`: the reference, the units' factors, the sum.  Nothing is set before the first chunk: these warps have no
+        // barrier behind them yet, so a value another thread stored could land on top of theirs
+        if (warp < G) {
             float m[CHUNK / 32], l[CHUNK / 32];
 #pragma unroll
             for (int x = 0; x < CHUNK / 32; ++x) {
