@@ -493,12 +493,13 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
             const int32_t *pt = A.page_table + (int64_t)u.seq * A.max_pages;
             const uint8_t *kv = A.pool + A.layer * A.geo.layer_stride + (int64_t)u.head * A.geo.page_bytes + B_SCALES_OFF;
             // What a step needs of its tiles' scales is the same for every row: lane i works it out for step i of 32, and a
-            // step takes it from there.  rec_k: this half's K scale, negative where the page is not there.  rec_v: E of the
+            // step takes it from there.  rec_k: this half's K scale, -1 where the page is not there and 0 past the sequence's
+            // end, where the pool may hold anything (a sign of its own for one half's page would clear the other's V).  rec_v: E of the
             // step (its largest V exponent so far) in the high half, the exponent of this half's weights, V scale included,
             // in the low one.  The next 32 steps' page slots and scales are loaded while these are used.
             auto load_slot = [&](int j) { return j < nt ? ld_now(pt + ((u.k0 + j * PFB_KEYS) >> 8)) : -1; };
             auto load_scales = [&](int slot, int j) {
-                if (slot < 0 || slot >= A.geo.n_pages) return make_float4(-1.0f, 0.f, -1.0f, 0.f);
+                if (slot < 0 || slot >= A.geo.n_pages) return make_float4(0.f, 0.f, 0.f, 0.f);
                 return ld_now(reinterpret_cast<const float4 *>(kv + (int64_t)slot * A.geo.slot_stride + (((u.k0 >> 7) + j) & 1) * 16));
             };
             int slot = load_slot(lane);
@@ -521,7 +522,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
                     }
                     top = max(top, E);
                     const int ev = part ? eb : ea;
-                    rec_k = part ? sc.z : sc.x;
+                    const float dks = part ? (u.k0 + step * PFB_KEYS + BT < kv_end ? sc.z : 0.0f) : sc.x;
+                    rec_k = slot >= 0 && slot < A.geo.n_pages ? fmaxf(dks, 0.0f) : -1.0f;
                     rec_v = (top << 16) | ((ev == PF_NO_E ? -188 : max(ev - top, -200) + PF_SHIFT) & 0xFFFF);
                     slot = load_slot(step + 32);
                 }
