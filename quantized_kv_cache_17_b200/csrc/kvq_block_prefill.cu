@@ -75,9 +75,12 @@ __device__ __forceinline__ bool plan_ok(const PfbArgs &A) {
 // conversion of every K and V code to 16 bits, which would move as many bytes
 // through shared memory as the products themselves.
 // Weights: W = 2^(s - m) 2^(e_v - E) 2^10, with s the score in base 2, m the row's
-// reference, e_v the exponent of the tile's V scale and E the largest e_v of the
-// unit so far, so V scales cost nothing.  m moves only when a score passes it by
-// 2^5: then, or when E moves, the row's O is multiplied in TMEM.
+// reference, e_v the exponent of the tile's V scale, so V scales cost nothing, and
+// E the row's own: the largest s - m + e_v of the keys it attends to, rounded up.
+// So what a weight is measured by is the largest product of weight and V scale in
+// its row; large values that the row does not see, or that have no weight in it,
+// take no bits from the others.  References move only when a score, or a score and
+// its V exponent, pass theirs by 2^5: the row's O is then multiplied in TMEM.
 // TMEM: O 0-255, S 256-383, weights 384-479 (term i of the 32 keys c at
 // 384 + 24 c + 8 i); all 512 columns are allocated.  The scores of step j + 1 are
 // made as soon as the softmax has step j's in registers, behind the values of step
@@ -93,11 +96,12 @@ static_assert(2 * PF_REGS_SOFT + PF_REGS_REST <= 3 * PF_REGS, "the softmax warps
 constexpr int PF_SLOT_BYTES = 32768;
 constexpr uint64_t PF_WAIT_NS = 2000000000ull;
 constexpr int PF_S_COL = 256, PF_P_COL = 384;
-// m moves when a score passes it by 2^PF_LAZY; weights are made 2^PF_SHIFT times larger, up to fp16's 2^15.  At 3 and 12 the
+// References move when they are passed by 2^PF_LAZY; weights are made 2^PF_SHIFT times larger, up to fp16's 2^15.  At 3 and 12 the
 // first steps of a unit rescaled O about twice as often.
 constexpr int PF_LAZY = 5, PF_SHIFT = 10;
 static_assert(PF_LAZY + PF_SHIFT == 15, "the largest weight");
-constexpr int PF_NO_E = -10000;
+constexpr float PF_NO_E = -10000.0f;             // no key seen
+constexpr float PF_ZERO_V = -1000.0f;            // the exponent of a V scale of 0, whose codes are 0 too
 
 template <int TERMS> struct PfCfg {
     static constexpr int K_SLOTS = 2, V_SLOTS = TERMS == 2 ? 3 : 2;
@@ -111,7 +115,7 @@ struct PfTail {
     uint32_t tmem;
     int abort;
     float qscale[PFB_ROWS];
-    float red[2][PFB_ROWS];
+    float red[2][PFB_ROWS], ev[PF_SOFT];
 };
 static_assert(sizeof(PfTail) <= 2048, "tail");
 static_assert(PfCfg<2>::SMEM <= 232448 && PfCfg<3>::SMEM <= 232448, "227 KB a CTA");
@@ -494,9 +498,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
             const uint8_t *kv = A.pool + A.layer * A.geo.layer_stride + (int64_t)u.head * A.geo.page_bytes + B_SCALES_OFF;
             // What a step needs of its tiles' scales is the same for every row: lane i works it out for step i of 32, and a
             // step takes it from there.  rec_k: this half's K scale, -1 where the page is not there and 0 past the sequence's
-            // end, where the pool may hold anything (a sign of its own for one half's page would clear the other's V).  rec_v: E of the
-            // step (its largest V exponent so far) in the high half, the exponent of this half's weights, V scale included,
-            // in the low one.  The next 32 steps' page slots and scales are loaded while these are used.
+            // end, where the pool may hold anything (a sign of its own for one half's page would clear the other's V).  rec_v: the
+            // exponent of this half's V scale.  The next 32 steps' page slots and scales are loaded while these are used.
             auto load_slot = [&](int j) { return j < nt ? ld_now(pt + ((u.k0 + j * PFB_KEYS) >> 8)) : -1; };
             auto load_scales = [&](int slot, int j) {
                 if (slot < 0 || slot >= A.geo.n_pages) return make_float4(0.f, 0.f, 0.f, 0.f);
@@ -504,32 +507,22 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
             };
             int slot = load_slot(lane);
             float4 sc = load_scales(slot, lane);
-            float rec_k = 0.0f;
-            int rec_v = 0;
-            float m = -INFINITY, l = 0.0f;
-            int E = PF_NO_E;
+            float rec_k = 0.0f, rec_v = 0.0f;
+            float m = -INFINITY, l = 0.0f;               // the score's reference, and the sum of 2^(s - m)
+            float R = -INFINITY, E = PF_NO_E;            // the largest s + e_v, and ceil(R - m)
             for (int j = 0; j < nt; ++j, ++it) {
                 const int key0 = u.k0 + j * PFB_KEYS, mine = key0 + 64 * part;
                 if ((j & 31) == 0) {
                     const int step = j + lane;
-                    auto exponent = [](float x) { return x > 0.0f ? (int)(__float_as_uint(x) >> 23) - 127 : PF_NO_E; };
-                    const int ea = exponent(sc.y), eb = u.k0 + step * PFB_KEYS + BT < kv_end ? exponent(sc.w) : PF_NO_E;
-                    int top = step < nt ? max(ea, eb) : PF_NO_E;
-#pragma unroll
-                    for (int d = 1; d < 32; d <<= 1) {
-                        const int o = __shfl_up_sync(0xffffffffu, top, d);
-                        if (lane >= d) top = max(top, o);
-                    }
-                    top = max(top, E);
-                    const int ev = part ? eb : ea;
-                    const float dks = part ? (u.k0 + step * PFB_KEYS + BT < kv_end ? sc.z : 0.0f) : sc.x;
-                    rec_k = slot >= 0 && slot < A.geo.n_pages ? fmaxf(dks, 0.0f) : -1.0f;
-                    rec_v = (top << 16) | ((ev == PF_NO_E ? -188 : max(ev - top, -200) + PF_SHIFT) & 0xFFFF);
+                    const bool second = u.k0 + step * PFB_KEYS + BT < kv_end;
+                    const float dk = part ? (second ? sc.z : 0.0f) : sc.x, dv = part ? (second ? sc.w : 0.0f) : sc.y;
+                    rec_k = slot >= 0 && slot < A.geo.n_pages ? fmaxf(dk, 0.0f) : -1.0f;
+                    rec_v = dv > 0.0f ? (float)((int)(__float_as_uint(dv) >> 23) - 127) : PF_ZERO_V;
                     slot = load_slot(step + 32);
                 }
                 if ((j & 31) == 16) sc = load_scales(slot, (j & ~31) + 32 + lane);
                 const float dk = __shfl_sync(0xffffffffu, rec_k, j & 31);
-                const int rv = __shfl_sync(0xffffffffu, rec_v, j & 31), En = rv >> 16, c0 = (int)(short)(rv & 0xFFFF);
+                const float ev = __shfl_sync(0xffffffffu, rec_v, j & 31);
                 const bool there = !(dk < 0.0f);
                 wait_s(&X.s_full, it & 1);
                 tc_fence_after();
@@ -555,16 +548,19 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
                 for (int x = 0; x < 64; x += 2) mx4[(x >> 1) & 3] = max3(mx4[(x >> 1) & 3], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
                 float mx = max3(fmaxf(mx4[0], mx4[1]), mx4[2], mx4[3]);
                 mx *= f;                                                         // f > 0
-                if (pair_any(mx > m + (float)PF_LAZY || En > E, bar)) {
+                if (pair_any(mx > fminf(m, R - ev) + (float)PF_LAZY, bar)) {
                     X.red[part][row] = mx;
+                    if (lane == 0) X.ev[warp] = ev;
                     asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
                     // every row of the warp moves when one asks: moved alone, the others ask more often (3 to 6 % of a call)
-                    const float mn = fmaxf(m, fmaxf(X.red[0][row], X.red[1][row]));
+                    const float other = X.red[part ^ 1][row], mn = fmaxf(m, fmaxf(mx, other));
                     const float fm = m == -INFINITY ? 0.0f : ex2(m - mn);
+                    R = fmaxf(R, fmaxf(mx + ev, other + X.ev[warp ^ 4]));
+                    const float En = mn == -INFINITY ? E : ceilf(R - mn);        // no key yet: as it was
                     if (j > 0) {
                         wait_s(&X.o_done, (it - 1) & 1);
                         tc_fence_after();
-                        const float fo = fm * (E == PF_NO_E ? 0.0f : pow2f(E - En));
+                        const float fo = m == -INFINITY ? 0.0f : ex2((m - mn) + (E - En));
                         uint32_t o[32];
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
@@ -579,14 +575,14 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
                     m = mn;
                     E = En;
                 }
-                // The sum takes what the weights are made of.  A V scale so far below the largest (or 0) that the weights
-                // vanish would take the sum with it: it is made first then.
-                const float ref = m == -INFINITY ? 0.0f : m;
-                if (c0 < -28) {
+                // The sum takes what the weights are made of.  A V scale so small (or 0) that the weights vanish beside the
+                // row's others would take the sum with it: it is made first then.
+                const float ref = m == -INFINITY ? 0.0f : m, c0 = ev - E + (float)PF_SHIFT;
+                if (c0 < -28.0f) {
 #pragma unroll
                     for (int x = 0; x < 64; ++x) l += ex2(fmaf(__uint_as_float(s[x]), f, -ref));
                 }
-                const uint64_t f2 = pack_f2(f, f), b2 = pack_f2((float)c0 - ref, (float)c0 - ref);
+                const uint64_t f2 = pack_f2(f, f), b2 = pack_f2(c0 - ref, c0 - ref);
                 uint64_t sum[2] = {0, 0};
                 uint32_t t[48];
 #pragma unroll
@@ -607,10 +603,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
                         split_weights(h[0], h[1], t[24 * c + x], t[24 * c + 8 + x], t[24 * c + 16 + x]);
                     }
                 }
-                if (c0 >= -28) {
+                if (c0 >= -28.0f) {
                     float a0, a1;
                     unpack_f2(add_f2(sum[0], sum[1]), a0, a1);
-                    l += (a0 + a1) * pow2f(-c0);
+                    l = fmaf(a0 + a1, ex2(-c0), l);
                 }
                 if (j > 0) {                             // the weights before have been used
                     wait_s(&X.o_done, (it - 1) & 1);
@@ -653,7 +649,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) block_prefill_kernel(PfbArgs A)
             asm volatile("bar.sync %0, 64;" ::"r"(bar) : "memory");
             l = X.red[0][row] + X.red[1][row];
             const bool cut = u.slot >= 0;
-            const float unit_o = E == PF_NO_E ? 0.0f : exp2f((float)(E - PF_SHIFT));
+            const float unit_o = E == PF_NO_E ? 0.0f : exp2f(E - (float)PF_SHIFT);
             const float fo = cut ? unit_o : (l == 0.0f ? 0.0f : unit_o / l);   // NaN stays NaN
             const int tok = r / A.G;
             const int64_t at = r < n_rows ? ((int64_t)(u.row_start + tok) * A.n_q_heads + u.head * A.G + (r - tok * A.G)) * D : -1;
