@@ -9,11 +9,13 @@
 //   S[8 heads][16 tokens] = Q K^T, m16n8k16 in fp16.  Codes are exact in fp16.
 //     The query rows are fp16 high parts (rows 0-7) and low parts (rows 8-15) of
 //     q 2^kq, so the product keeps 22 bits of q at no extra instruction.
-//   softmax in base 2 with a running maximum per head that moves only when a
-//     score passes it by 2^8 (the weights then stay below 2^8).
-//   O[256 dims][8 heads] += V^T W, W = p d_v as an fp16 pair (high, low): V codes
-//     are the A operand as they are, and d_v, a power of two, goes into W relative
-//     to the largest d_v the warp has met.
+//   softmax in base 2 with a running maximum m per head that moves only when a
+//     score passes it by 2^8.
+//   O[256 dims][8 heads] += V^T W, W = p d_v 2^(7 - E) as an fp16 pair (high, low):
+//     V codes are the A operand as they are, and d_v, a power of two, goes into W.
+//     E is the head's own: the largest log2(p d_v) that the warp has met, rounded
+//     up, which moves as m does.  Large values without weight take no bits from the
+//     others.
 // The scores' C fragment is the values' B fragment: with column n of score tile j
 // holding token 4 (n >> 1) + 2 j + (n & 1), lane (g, t) ends up with the tokens
 // 4t .. 4t + 3 of head g, four adjacent bytes of a V row.
@@ -33,6 +35,7 @@ static_assert(BD_SETS * BD_REGS_COMPUTE + BD_REGS_REST <= 4 * BD_REGS, "the comp
 // waits for.
 constexpr int BD_STAGES = 6;
 static_assert(BD_STAGES % BD_SETS == 0, "stages per set");
+constexpr float BD_ZERO_V = -1000.0f;                 // the exponent of a V scale of 0, whose codes are 0 too
 constexpr uint64_t BD_WAIT_NS = 2000000000ull;
 constexpr int BD_RING = BD_STAGES * BT_BYTES;
 struct BdTail {                                   // after the ring
@@ -214,7 +217,7 @@ __global__ void __launch_bounds__(BD_THREADS, 1) block_decode_kernel(BdArgs A) {
 #pragma unroll
         for (int x = 0; x < 16; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.0f;
         float m = -INFINITY, l = 0.0f;             // of head g; l over this lane's tokens
-        int E = -10000;                            // o is in units of 2^(E - 7)
+        float R = -INFINITY, E = 0.0f;             // the largest score and V exponent together, and ceil(R - m); o is in units of 2^(E - 7)
         for (int j = (set + BD_SETS - it % BD_SETS) % BD_SETS; j < n_tiles && alive; j += BD_SETS) {
             const int s = (it + j) % BD_STAGES;
             if (!__all_sync(0xffffffffu, mbar_wait_bounded(&T.full[s], ((it + j) / BD_STAGES) & 1, BD_WAIT_NS))) {
@@ -276,15 +279,19 @@ __global__ void __launch_bounds__(BD_THREADS, 1) block_decode_kernel(BdArgs A) {
                 float mx = fmaxf(fmaxf(p[0], p[1]), fmaxf(p[2], p[3]));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const int ev = dv > 0.0f ? (int)(__float_as_uint(dv) >> 23) - 127 : -10000;
-                if (__any_sync(0xffffffffu, mx > m + 8.0f) || ev > E) {
-                    const float mn = mx > m + 8.0f ? mx : m;      // only heads that ask move
-                    const float fm = m == mn ? 1.0f : (m == -INFINITY ? 0.0f : exp2f(m - mn));
-                    const float fe = ev > E ? pow2i(E - ev) : 1.0f;
-                    m = mn;
-                    E = max(E, ev);
-                    l *= fm;
-                    const float f0 = __shfl_sync(0xffffffffu, fm, 8 * t) * fe, f1 = __shfl_sync(0xffffffffu, fm, 8 * t + 4) * fe;
+                const float ev = dv > 0.0f ? (float)((int)(__float_as_uint(dv) >> 23) - 127) : BD_ZERO_V;
+                const bool ask = mx > fminf(m, R - ev) + 8.0f;
+                if (__any_sync(0xffffffffu, ask)) {
+                    float fo = 1.0f;
+                    if (ask) {                                    // only heads that ask move
+                        const float mn = fmaxf(m, mx), Rn = fmaxf(R, mx + ev), En = ceilf(Rn - mn);
+                        fo = m == -INFINITY ? 0.0f : exp2f((m - mn) + (E - En));
+                        l *= m == -INFINITY ? 0.0f : exp2f(m - mn);
+                        m = mn;
+                        R = Rn;
+                        E = En;
+                    }
+                    const float f0 = __shfl_sync(0xffffffffu, fo, 8 * t), f1 = __shfl_sync(0xffffffffu, fo, 8 * t + 4);
 #pragma unroll
                     for (int x = 0; x < 16; ++x) {
                         o[x][0] *= f0;
@@ -293,17 +300,17 @@ __global__ void __launch_bounds__(BD_THREADS, 1) block_decode_kernel(BdArgs A) {
                         o[x][3] *= f1;
                     }
                 }
-                const float mref = m == -INFINITY ? 0.0f : m;
-                const float wv = ev < -5000 ? 0.0f : pow2i(ev - E + 7);
+                const float mref = m == -INFINITY ? 0.0f : m, c = ev - E + 7.0f;
                 uint32_t whi[2], wlo[2];
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const float p0 = ex2(p[2 * y] - mref), p1 = ex2(p[2 * y + 1] - mref);
-                    l += p0 + p1;
-                    const __half2 h = __floats2half2_rn(p0 * wv, p1 * wv);
+                    const float s0 = p[2 * y] - mref, s1 = p[2 * y + 1] - mref;
+                    l += ex2(s0) + ex2(s1);
+                    const float w0 = ex2(s0 + c), w1 = ex2(s1 + c);      // not 2^s0 2^c: 2^s0 alone may be too small to hold
+                    const __half2 h = __floats2half2_rn(w0, w1);
                     const float2 r = __half22float2(h);
                     whi[y] = h2_as_u32(h);
-                    wlo[y] = h2_as_u32(__floats2half2_rn(p0 * wv - r.x, p1 * wv - r.y));
+                    wlo[y] = h2_as_u32(__floats2half2_rn(w0 - r.x, w1 - r.y));
                 }
                 const uint32_t keep = valid == 4 ? 0xFFFFFFFFu : (1u << (8 * valid)) - 1u;   // codes past the end may be NaN
 #pragma unroll
@@ -329,7 +336,6 @@ __global__ void __launch_bounds__(BD_THREADS, 1) block_decode_kernel(BdArgs A) {
         sync();
         // ---- merge of the warps: each brings its o to the unit's reference (true units: 2^(E - 7)) ----
         {
-            const float eo = E > -5000 ? exp2f((float)(E - 7)) : 0.0f;
             float f[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
@@ -337,7 +343,8 @@ __global__ void __launch_bounds__(BD_THREADS, 1) block_decode_kernel(BdArgs A) {
 #pragma unroll
                 for (int w = 1; w < BD_WARPS; ++w) M = fmaxf(M, T.m[w][2 * t + x]);
                 const float mine = T.m[warp][2 * t + x];
-                f[x] = mine == -INFINITY ? 0.0f : ex2(mine - M) * eo;
+                const float eo = __shfl_sync(0xffffffffu, E, 8 * t + 4 * x) - 7.0f;
+                f[x] = mine == -INFINITY ? 0.0f : exp2f(mine - M + eo);
             }
             if (tid < 8) {                         // head tid: the reference and the sum, for later
                 float M = T.m[0][tid], L = 0.0f;

@@ -207,3 +207,28 @@ def test_prefill_of_values_of_random_sizes(spread):
     q = value_queries(rng, sum(toks), 12, "bf16")
     _, of = prefill(make_pool(cache, 12), q, dev(table), pos0, toks)
     check_rows(cache, table, pos0, toks, q, of, torch.bfloat16)
+
+
+@pytest.mark.parametrize("n_ctas", [1, 148])
+@pytest.mark.parametrize("ladder", list(LADDERS))
+def test_decode_of_values_of_very_different_sizes(ladder, n_ctas):
+    rng = np.random.default_rng(250)
+    end = 64 * len(LADDERS[ladder])
+    cache, table = ladder_cache(rng, ladder)
+    lens = [end - 3, max(64, end - 64)]
+    q = value_queries(rng, 2, 4, "f32")
+    _, of = decode(make_pool(cache, 4), q, dev(table), lens, n_ctas=n_ctas)
+    for b, n in enumerate(lens):
+        check_rows(cache, table[b:b + 1], [n - 1], [1], q[b:b + 1], of[b:b + 1])
+
+
+@pytest.mark.parametrize("spread", [20, 60])
+def test_decode_of_values_of_random_sizes(spread):
+    rng = np.random.default_rng(260)
+    lens = [2070, 400, 977]
+    cache, table = random_sizes_cache(rng, spread, lens)
+    q = value_queries(rng, 3, 12, "f32")
+    for n_ctas in (3, 148):
+        _, of = decode(make_pool(cache, 12), q, dev(table), lens, n_ctas=n_ctas)
+        for b, n in enumerate(lens):
+            check_rows(cache, table[b:b + 1], [n - 1], [1], q[b:b + 1], of[b:b + 1])
