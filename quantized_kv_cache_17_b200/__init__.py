@@ -266,12 +266,42 @@ def paged_decode_attn_q4_0_noalloc(pool: KVPool, layer: int, q, page_table, plan
            "paged_decode_attn_q4_0_noalloc")
 
 
+def _check_block_decode(what, pool, q, page_table, plan_dev, info, workspace, out_bf16, out_f32, status):
+    """The tensors of an fp8b decode: types, lengths, device."""
+    torch = _torch()
+    f32, i32, n_seq, heads = torch.float32, torch.int32, info.n_seq, pool.desc.n_q_heads
+    n = n_seq * heads * HEAD_DIM
+    if q.dtype is not f32:                           # what kv_append_rope returns for 16-bit rows unless asked for fp32
+        raise KVQError(f"{what}: q is {q.dtype}, want float32 (kv_append_rope: q_out_dtype=torch.float32)")
+    if not q.is_contiguous() or q.numel() < n:
+        raise KVQError(f"{what}: q is not contiguous [{n_seq}, {heads}, {HEAD_DIM}]")
+    if page_table.dtype is not i32 or not page_table.is_contiguous() or page_table.size(0) < n_seq:
+        raise KVQError(f"{what}: page_table is contiguous int32 with a row for each of the plan's sequences")
+    if plan_dev.dtype is not i32 or not plan_dev.is_contiguous() or plan_dev.numel() < info.plan_len:
+        raise KVQError(f"{what}: plan_dev is the whole plan, contiguous int32")
+    if not workspace.is_contiguous():
+        raise KVQError(f"{what}: workspace is not contiguous")
+    if out_bf16 is not None and (out_bf16.element_size() != 2 or out_bf16.dtype is torch.float16 or
+                                 not out_bf16.is_contiguous() or out_bf16.numel() < n):
+        raise KVQError(f"{what}: out_bf16 is contiguous, shaped as q and bfloat16 (or 16-bit integers)")
+    if out_f32 is not None and (out_f32.dtype is not f32 or not out_f32.is_contiguous() or out_f32.numel() < n):
+        raise KVQError(f"{what}: out_f32 is contiguous, shaped as q and float32")
+    if status is not None:
+        _check_status(what, status)
+    _on_current_device(what, pool.buf, q, page_table, plan_dev, workspace, out_bf16, out_f32, status)
+
+
+def _check_status(what, status):
+    if status.dtype is not _torch().int32 or status.numel() < 1:
+        raise KVQError(f"{what}: status is an int32 tensor")
+
+
 def paged_decode_attn_combined(pool: KVPool, layer: int, q, page_table, plan_dev, info: PlanInfo, workspace,
                                out_bf16, out_f32=None, status=None, stream=None):
     """Decode with the combine fused in; workspace must have been zero-filled
     once before its first use (the call leaves its counters at zero)."""
     if pool.fmt == FP8B:
-        _on_current_device("paged_decode_attn_fp8b_combined", pool.buf, q, page_table, plan_dev, workspace, out_bf16, out_f32, status)
+        _check_block_decode("paged_decode_attn_fp8b_combined", pool, q, page_table, plan_dev, info, workspace, out_bf16, out_f32, status)
     cp = pool.c_pool()
     name = _DECODE[pool.fmt] + "_combined"
     _check(getattr(lib(), name)(ctypes.byref(cp), layer, _ptr(q), _ptr(page_table), page_table.shape[1],
@@ -303,7 +333,7 @@ def paged_decode_attn(pool: KVPool, layer: int, q, page_table, plan_dev, info: P
     """Split-K decode attention of the pool's format (tensor-core kernel, or
     the CUDA-core control when cudacore=True); partials go to workspace."""
     if pool.fmt == FP8B:
-        _on_current_device("paged_decode_attn_fp8b", pool.buf, q, page_table, plan_dev, workspace, status)
+        _check_block_decode("paged_decode_attn_fp8b", pool, q, page_table, plan_dev, info, workspace, None, None, status)
     cp = pool.c_pool()
     args = (ctypes.byref(cp), layer, _ptr(q), _ptr(page_table), page_table.shape[1], _ptr(plan_dev),
             ctypes.byref(info), _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
@@ -340,6 +370,7 @@ def paged_decode_attn_nvfp4(pool, layer, q, page_table, plan_dev, info, workspac
 
 
 def paged_decode_attn_fp8b(pool, layer, q, page_table, plan_dev, info, workspace, status=None, stream=None):
+    """q is fp32, as for the other formats; of kv_append_rope's rows ask for it with q_out_dtype."""
     assert pool.fmt == FP8B
     paged_decode_attn(pool, layer, q, page_table, plan_dev, info, workspace, status, stream)
 
@@ -392,8 +423,9 @@ def kv_append_rope(pool: KVPool, layer: int, k, v, row_start, pos0, page_table, 
     ([n_rows, n_q_heads, 256] of the same type) likewise.  Sequence s owns rows
     row_start[s] .. row_start[s+1] - 1 at positions pos0[s] ..; row_start, pos0 and
     page_table are device int32.  Returns the rotated q (q_out, or a new tensor of
-    type q_out_dtype: fp32, or q's own type for fp8b pools; by default fp32 except
-    that fp8b keeps q's type; rows past row_start[-1] are not written), None without
+    type q_out_dtype: fp32, which every decode takes, or q's own type for fp8b pools,
+    which the prefill takes; by default fp32 except that fp8b keeps q's type; rows
+    past row_start[-1] are not written), None without
     q.  k and v may both be None."""
     torch = _torch()
     d = pool.desc
@@ -439,6 +471,8 @@ def kv_append_rope(pool: KVPool, layer: int, k, v, row_start, pos0, page_table, 
         if cos_sin.dtype is not torch.float32 or not cos_sin.is_contiguous():
             raise KVQError("kv_append_rope: cos_sin is not a contiguous float32 tensor")
         cp_ = cos_sin.data_ptr()
+    if status is not None:
+        _check_status("kv_append_rope", status)
     _on_current_device("kv_append_rope", pool.buf, first, v, q, q_out, row_start, pos0, page_table, cos_sin, status)
     rc = lib().kv_append_rope(ctypes.byref(pool.c_pool()), layer, cp_, n_pos, rot, 1 if interleaved else 0, qp, kp, vp, dt, qs,
                               ks, vs, n_rows, rs, p0, pt, max_pages, n_seq, op, odt, None if status is None else status.data_ptr(),
@@ -487,6 +521,10 @@ def paged_prefill_attn_fp8b(pool: KVPool, layer: int, q, page_table, plan_dev, i
     pt, pl = _index(page_table, "page_table"), _index(plan_dev, "plan_dev")
     if plan_dev.shape[0] < info.plan_len:
         raise KVQError(f"{what}: plan_dev is shorter than the plan")
+    if workspace is not None and not workspace.is_contiguous():
+        raise KVQError(f"{what}: workspace is not contiguous")
+    if status is not None:
+        _check_status(what, status)
     _on_current_device(what, pool.buf, q, page_table, plan_dev, workspace, out_bf16, out_f32, status)
     cp = pool.c_pool()
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()

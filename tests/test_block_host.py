@@ -224,3 +224,43 @@ def test_binding_refuses_wrong_tensors():
     q = torch.zeros((3, 24, 256), dtype=torch.bfloat16)
     with pytest.raises(kvq.KVQError):
         kvq.paged_prefill_attn_fp8b(pool, 0, q, pt, None, info, None, q)
+
+
+def _decode_call(**kw):
+    """A decode through the binding with CPU tensors: what it refuses before it looks at the device."""
+    import torch
+    desc = _pool().desc
+    plan, info = kvq.decode_plan(desc, [1000, 70], max_pages=8, n_ctas=148)
+    a = dict(q=torch.zeros((2, 24, 256)), page_table=torch.zeros((2, 8), dtype=torch.int32), plan_dev=torch.from_numpy(plan),
+             workspace=torch.zeros(info.workspace_bytes // 4), out_bf16=torch.zeros((2, 24, 256), dtype=torch.bfloat16), out_f32=None,
+             status=torch.zeros(1, dtype=torch.int32))
+    a.update(kw)
+    pool = kvq.KVPool(desc, torch.zeros(16, dtype=torch.uint8))
+    outs = (a.pop("out_bf16"), a.pop("out_f32"))
+    for call in (lambda: kvq.paged_decode_attn_combined(pool, 0, a["q"], a["page_table"], a["plan_dev"], info, a["workspace"], *outs,
+                                                        a["status"]),
+                 lambda: kvq.paged_decode_attn_fp8b(pool, 0, a["q"], a["page_table"], a["plan_dev"], info, a["workspace"], a["status"])):
+        try:
+            call()
+        except kvq.KVQError as e:
+            yield str(e)
+
+
+def test_binding_refuses_wrong_tensors_of_a_decode():
+    import torch
+    assert all("the current device" in m for m in _decode_call())              # nothing else is wrong with these
+    for t in (torch.bfloat16, torch.float16, torch.float64):                   # a 16-bit query is not read as fp32, past its end
+        msgs = list(_decode_call(q=torch.zeros((2, 24, 256), dtype=t)))
+        assert len(msgs) == 2 and all("float32" in m for m in msgs)
+    for kw, word in ((dict(q=torch.zeros((1, 24, 256))), "q is not"), (dict(q=torch.zeros((2, 24, 512))[..., :256]), "q is not"),
+                     (dict(page_table=torch.zeros((1, 8), dtype=torch.int32)), "page_table"),
+                     (dict(page_table=torch.zeros((2, 8), dtype=torch.int64)), "page_table"),
+                     (dict(plan_dev=torch.zeros(20, dtype=torch.int32)), "plan_dev"),
+                     (dict(plan_dev=torch.zeros(4096, dtype=torch.float32)), "plan_dev"),
+                     (dict(workspace=torch.zeros(1 << 20)[::2]), "workspace"), (dict(status=torch.zeros(1)), "status")):
+        msgs = list(_decode_call(**kw))
+        assert len(msgs) == 2 and all(word in m for m in msgs), (kw.keys(), msgs)
+    for kw in (dict(out_bf16=torch.zeros((2, 24, 256))), dict(out_bf16=torch.zeros((2, 24, 256), dtype=torch.float16)),
+               dict(out_bf16=torch.zeros((1, 24, 256), dtype=torch.bfloat16)), dict(out_f32=torch.zeros((2, 24, 256), dtype=torch.bfloat16)),
+               dict(out_f32=torch.zeros((2, 24, 128)))):
+        assert "shaped as q" in list(_decode_call(**kw))[0]

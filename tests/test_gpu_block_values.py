@@ -232,3 +232,29 @@ def test_decode_of_values_of_random_sizes(spread):
         _, of = decode(make_pool(cache, 12), q, dev(table), lens, n_ctas=n_ctas)
         for b, n in enumerate(lens):
             check_rows(cache, table[b:b + 1], [n - 1], [1], q[b:b + 1], of[b:b + 1])
+
+
+def test_decode_takes_the_query_of_an_append():
+    """fp32 when asked for; the append's default for 16-bit rows, which the prefill takes, is refused."""
+    rng = np.random.default_rng(270)
+    x = dev(rng.standard_normal((2, 16, 256)).astype(np.float32), torch.bfloat16)
+    q, k, v = x[:, :12], x[:, 12:14], x[:, 14:]
+    table = np.array([[1], [0]], np.int32)
+    cs, td = br.rope_table(10, 64), dev(table)
+    pool = kvq.KVPool.allocate(kvq.make_desc(1, 2, 12, 2, "fp8b"))
+    args = (pool, 0, k, v, i32([0, 1, 2]), i32([0, 0]), td)
+    default = kvq.kv_append_rope(*args, cos_sin=dev(cs), q=q)
+    plan, info = kvq.decode_plan(pool.desc, [1, 1], 1)
+    ws, out = torch.empty(info.workspace_bytes // 4, device="cuda"), torch.empty((2, 12, 256), dtype=torch.bfloat16, device="cuda")
+    assert default.dtype == torch.bfloat16
+    with pytest.raises(kvq.KVQError, match="float32"):
+        kvq.paged_decode_attn_combined(pool, 0, default, td, dev(plan), info, ws, out)
+    with pytest.raises(kvq.KVQError, match="float32"):
+        kvq.paged_decode_attn_fp8b(pool, 0, default, td, dev(plan), info, ws)
+    qf = kvq.kv_append_rope(*args, cos_sin=dev(cs), q=q, q_out_dtype=torch.float32)
+    kvq.paged_decode_attn_combined(pool, 0, qf, td, dev(plan), info, ws, out)
+    cache = br.Cache.unpack(pool.buf.view(2, 2, br.PAGE_BYTES).cpu().numpy())
+    for b in range(2):                                       # one key: its value
+        for h in range(2):
+            want = torch.from_numpy(cache.values(table[b], 1, h)[1].astype(np.float32)).to(torch.bfloat16)
+            assert torch.equal(out[b, 6 * h:6 * h + 6].cpu(), want.expand(6, 256))
