@@ -424,8 +424,9 @@ int kvq_prefill_split(const kvq_pool_desc *desc, int pos0, int n_tok, int n_sms,
  *            NULL together (rotate q only), or q (append only)
  *  row_start device int32 [n_seq + 1]: sequence s owns the rows row_start[s] ..
  *            row_start[s+1] - 1 (possibly none), at the positions pos0[s],
- *            pos0[s] + 1, ...  Rows from row_start[n_seq] to n_rows - 1 are
- *            padding: neither read into the cache nor written to q_out
+ *            pos0[s] + 1, ...  Rows below row_start[0] and from row_start[n_seq]
+ *            to n_rows - 1 are padding: neither read into the cache nor written
+ *            to q_out
  *  pos0      device int32 [n_seq]: the sequence's length before the call
  *  q_out     device [n_rows][n_q_heads][256], contiguous, of type q_dtype:
  *            KVQ_F32, or dtype itself when the pool is fp8b.  May be q when the
@@ -437,7 +438,8 @@ int kvq_prefill_split(const kvq_pool_desc *desc, int pos0, int n_tok, int n_sms,
  * of kv_append for the rotated rows.
  * A page slot or a position out of range (of the page table, or of the cos_sin
  * table) sets KVQ_STATUS_BAD_SLOT and skips the rows concerned; a row_start that
- * decreases or passes n_rows sets KVQ_STATUS_BAD_PLAN.  Two sequences of the
+ * begins below 0, decreases or passes n_rows sets KVQ_STATUS_BAD_PLAN (what the
+ * call then appends and rotates is not defined).  Two sequences of the
  * batch must not append to the same page.  KVQ_EALIGN for a pointer or a row
  * stride that is not a multiple of 16 bytes. */
 int kv_append_rope(const kvq_pool *pool, int layer, const float *cos_sin, int n_pos, int rot_dim, int interleaved,

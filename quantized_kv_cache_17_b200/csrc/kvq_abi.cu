@@ -527,7 +527,7 @@ int kv_append_rope(const kvq_pool *pool, int layer, const float *cos_sin, int n_
     const int n_q = pool->desc.n_q_heads;
     // keeps the grid and the row arithmetic in range; row_start is int32
     if (n_rows > (1 << 26) || n_seq > (1 << 24) || n_rows * n_q > ((int64_t)1 << 31) ||
-        (n_rows / 64 + 2 * (int64_t)n_seq) * geo.n_kv_heads * 2 + (n_rows * n_q + 63) / 64 > INT32_MAX)
+        (n_rows / 64 + 2 * (int64_t)n_seq) * geo.n_kv_heads * 2 + (n_rows * n_q + 63) / 64 >= INT32_MAX)
         return KVQ_EINVAL;
     if ((k && (k_stride < (int64_t)geo.n_kv_heads * D || v_stride < (int64_t)geo.n_kv_heads * D)) ||
         (q && q_stride < (int64_t)n_q * D))

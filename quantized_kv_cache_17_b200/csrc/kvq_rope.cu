@@ -105,12 +105,24 @@ __device__ __forceinline__ void rope_row(float (&x)[8], const RopeArgs &R, const
     }
 }
 
-// Sequence and position of a row (by the whole warp).  False past the last
-// sequence's rows, and with a status bit where row_start or the position is bad.
+// The last block of a launch looks at row_start as a whole: no other block sees
+// more of it than its own rows need.
+__device__ __forceinline__ void check_row_start(const RopeArgs &R) {
+    bool bad = false;
+    for (int s = threadIdx.x; s <= R.n_seq; s += blockDim.x) {
+        const int at = __ldg(R.row_start + s);
+        bad |= at < (s > 0 ? __ldg(R.row_start + s - 1) : 0) || at > R.n_rows;
+    }
+    if (bad) status_or(R.status, KVQ_STATUS_BAD_PLAN);
+}
+
+// Sequence and position of a row (by the whole warp).  False outside all
+// sequences' rows, and with a status bit where row_start or the position is bad.
 __device__ __forceinline__ bool row_place(const RopeArgs &R, int64_t row, int lane, int &seq, int &pos) {
     if (row >= __ldg(R.row_start + R.n_seq)) return false;
     seq = warp_find_last(R.n_seq, row, lane, [&](int s) { return (int64_t)__ldg(R.row_start + s); });
-    if (seq < 0 || row >= __ldg(R.row_start + seq + 1)) {
+    if (seq < 0) return false;
+    if (row >= __ldg(R.row_start + seq + 1)) {
         if (lane == 0) status_or(R.status, KVQ_STATUS_BAD_PLAN);
         return false;
     }
@@ -149,6 +161,7 @@ template <int FMT, typename T>
 __global__ void __launch_bounds__(128) rope_append_kernel(uint8_t *pool, PoolGeom geo, RopeArgs R, unsigned kv_blocks) {
     grid_dependency_wait();
     const int lane = threadIdx.x & 31;
+    if (blockIdx.x == gridDim.x - 1) return check_row_start(R);
     if (blockIdx.x >= kv_blocks) {
         rope_query<Fmt<FMT>::KROT, T, float>(R, (int64_t)(blockIdx.x - kv_blocks) * 4 + (threadIdx.x >> 5), lane);
         return;
@@ -353,17 +366,15 @@ template <typename T, typename TQ, int N> __device__ __forceinline__ void rope_q
         }
     }
     // positions: lane y < n has item y's, -1 where it has none
-    int seq = warp_find_last(R.n_seq, row0, lane, [&](int s) { return (int64_t)__ldg(R.row_start + s); });
+    int seq = warp_find_last(R.n_seq, row0, lane, [&](int s) { return (int64_t)__ldg(R.row_start + s); });   // -1: before all of them
     int pos = -1;
     if (lane < n) {
         const int row = (int)((item0 + lane) / n_q);
         if (row < __ldg(R.row_start + R.n_seq)) {
-            bool found = seq >= 0;
-            while (found && row >= __ldg(R.row_start + seq + 1))
-                if (++seq >= R.n_seq) found = false;
-            if (!found || row < __ldg(R.row_start + seq)) {
+            while (seq < R.n_seq && row >= __ldg(R.row_start + seq + 1)) ++seq;
+            if (seq >= R.n_seq || (seq >= 0 && row < __ldg(R.row_start + seq))) {
                 status_or(R.status, KVQ_STATUS_BAD_PLAN);
-            } else {
+            } else if (seq >= 0) {
                 const int64_t p = (int64_t)__ldg(R.pos0 + seq) + (row - __ldg(R.row_start + seq));
                 if (p < 0 || p >= (int64_t)R.max_pages * PAGE || (R.rot_dim && p >= R.n_pos)) status_or(R.status, KVQ_STATUS_BAD_SLOT);
                 else pos = (int)p;
@@ -426,6 +437,7 @@ __global__ void __launch_bounds__(BA_THREADS, 2) block_append_kernel(uint8_t *po
     __shared__ __align__(16) uint8_t s_v[32 * 528];     // V codes: 512 bytes a dim group, 16 of padding
     grid_dependency_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (blockIdx.x == gridDim.x - 1) return check_row_start(R);
     if (blockIdx.x >= kv_blocks) {
         const uint32_t item0 = ((blockIdx.x - kv_blocks) * BA_WARPS + warp) * q_rows;
         if (q_rows <= BA_ROWS) rope_queries<T, TQ, BA_ROWS>(R, item0, q_rows, lane);
@@ -439,10 +451,7 @@ __global__ void __launch_bounds__(BA_THREADS, 2) block_append_kernel(uint8_t *po
     const int seq = few      ? (by_row ? all.last_below(item) : all.last_tiles_below(item))
                     : by_row ? warp_find_last(R.n_seq, item, lane, [&](int s) { return (int64_t)__ldg(R.row_start + s); })
                              : warp_find_last(R.n_seq, item, lane, [&](int s) { return (int64_t)(__ldg(R.row_start + s) >> 6) + 2 * (int64_t)s; });
-    if (seq < 0) {
-        if (threadIdx.x == 0) status_or(R.status, KVQ_STATUS_BAD_PLAN);
-        return;
-    }
+    if (seq < 0) return;                                 // before the first sequence's rows
     const int row0 = few ? __shfl_sync(0xffffffffu, all.start, seq) : __ldg(R.row_start + seq);
     const int row1 = few ? __shfl_sync(0xffffffffu, all.start, seq + 1) : __ldg(R.row_start + seq + 1);
     const int p0 = few ? __shfl_sync(0xffffffffu, all.pos0, seq) : __ldg(R.pos0 + seq);
@@ -604,7 +613,7 @@ cudaError_t launch_typed(int fmt, uint8_t *pool, const PoolGeom &geo, const Rope
         // heads: 2,000 rows 15.6 and 15.7 us, 3,000 rows 22.2 and 21.7, 8,917 rows 60.7 and 55)
         const int q_rows = q_items <= BA_FEW ? 1 : sizeof(T) == 2 && q_items > 12 * BA_FEW ? BA_MANY : BA_ROWS;
         const int64_t qb = (q_items + BA_WARPS * q_rows - 1) / (BA_WARPS * q_rows);
-        return launch_ex(block_append_kernel<T, TQ>, dim3((unsigned)(kv + qb)), dim3(BA_THREADS), 0, s, false, pool, geo,
+        return launch_ex(block_append_kernel<T, TQ>, dim3((unsigned)(kv + qb + 1)), dim3(BA_THREADS), 0, s, false, pool, geo,
                          R, (unsigned)kv, by_row, q_rows);
     }
     if constexpr (std::is_same_v<TQ, float>) {           // the decodes of these formats take fp32 queries
@@ -614,7 +623,7 @@ cudaError_t launch_typed(int fmt, uint8_t *pool, const PoolGeom &geo, const Rope
                     : fmt == KVQ_K8V4  ? rope_append_kernel<KVQ_K8V4, T>
                     : fmt == KVQ_FP8   ? rope_append_kernel<KVQ_FP8, T>
                                        : rope_append_kernel<KVQ_NVFP4, T>;
-        return launch_ex(kern, dim3((unsigned)(kv + qb)), dim3(128), 0, s, false, pool, geo, R, (unsigned)kv);
+        return launch_ex(kern, dim3((unsigned)(kv + qb + 1)), dim3(128), 0, s, false, pool, geo, R, (unsigned)kv);
     } else {
         return cudaErrorNotSupported;
     }
