@@ -545,11 +545,11 @@ cudaError_t launch_block_decode(const uint8_t *pool, const PoolGeom &geo, int la
                    status, out_bf16, out_f32};
     cudaError_t e = launch_ex(block_decode_kernel, dim3((unsigned)n_ctas), dim3(BD_THREADS), BD_SMEM, s, false, a);
     if (e != cudaSuccess || !out_bf16 || info.n_units == info.n_seq * info.n_kv_heads) return e;
-    // few ranges, each cut into many units, are merged by 16 or 4 CTAs each, many by one: as many as fit the 148 SMs at once
+    // few ranges, each cut into many units, are merged by 16 or 4 CTAs each, many by one: as many as fit the SMs at once
     // (1 x 32,768 tokens of four KV heads: 21.3 us with 4, 20.1 with 16; 48 ragged sequences of two: 54 us with 4, 48 with 1)
-    const int groups = info.n_seq * info.n_kv_heads;
-    if (groups <= 148 / 16) return launch_ex(block_merge_kernel<16>, dim3((unsigned)groups * 16), dim3(BM_THREADS), 0, s, false, a);
-    if (groups <= 148 / 4) return launch_ex(block_merge_kernel<4>, dim3((unsigned)groups * 4), dim3(BM_THREADS), 0, s, false, a);
+    const int groups = info.n_seq * info.n_kv_heads, sms = device_sms();
+    if (groups <= sms / 16) return launch_ex(block_merge_kernel<16>, dim3((unsigned)groups * 16), dim3(BM_THREADS), 0, s, false, a);
+    if (groups <= sms / 4) return launch_ex(block_merge_kernel<4>, dim3((unsigned)groups * 4), dim3(BM_THREADS), 0, s, false, a);
     return launch_ex(block_merge_kernel<1>, dim3((unsigned)groups), dim3(BM_THREADS), 0, s, false, a);
 }
 

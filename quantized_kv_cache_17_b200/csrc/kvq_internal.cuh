@@ -148,6 +148,12 @@ struct PoolGeom {
     int n_pages, n_kv_heads;
 };
 
+// SMs of the current device; 148 if it cannot be asked.
+inline int device_sms() {
+    int dev = 0, sms = 0;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess ? sms : 148;
+}
+
 // Launch with programmatic stream serialisation (and, with coop, as a
 // cooperative launch: every block resident at once).
 template <typename... KArgs, typename... Args>

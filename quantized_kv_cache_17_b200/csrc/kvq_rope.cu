@@ -192,7 +192,6 @@ __global__ void __launch_bounds__(128) rope_append_kernel(uint8_t *pool, PoolGeo
 constexpr int BA_WARPS = 16, BA_THREADS = BA_WARPS * 32;
 constexpr int BA_ROWS = 4;             // rows of a warp, all loaded before the first is used
 constexpr int BA_MANY = 8;             // query items of a warp where there are many (16-bit types: fp32 ones would be spilled)
-constexpr int64_t BA_FEW = 4736;       // (row, head) items that get a warp each: 148 SMs x 2 CTAs x 16 warps
 constexpr int BA_DIRECT = 4;           // tokens of a tile up to which their V codes are stored byte by byte
 static_assert(BA_WARPS * BA_ROWS == BT && BA_ROWS == 4, "a CTA holds a tile's rows, a warp the tokens of one word of V codes");
 
@@ -608,10 +607,11 @@ cudaError_t launch_typed(int fmt, uint8_t *pool, const PoolGeom &geo, const Rope
         const int64_t by_tiles = (R.n_rows >> 6) + 2 * (int64_t)R.n_seq;
         const int by_row = R.n_rows < by_tiles ? 1 : 0;
         const int64_t kv = R.k ? (by_row ? R.n_rows : by_tiles) * geo.n_kv_heads * 2 : 0;
-        // a few query rows are spread over as many warps; more are taken BA_ROWS at a time, for the loads in flight and
+        // a few query rows are spread over as many warps, 2 CTAs of them an SM; more are taken BA_ROWS at a time, for the loads in flight and
         // the angles they share, and very many BA_MANY at a time, for the instructions around them (4 and 8 a warp, 24
         // heads: 2,000 rows 15.6 and 15.7 us, 3,000 rows 22.2 and 21.7, 8,917 rows 60.7 and 55)
-        const int q_rows = q_items <= BA_FEW ? 1 : sizeof(T) == 2 && q_items > 12 * BA_FEW ? BA_MANY : BA_ROWS;
+        const int64_t warps = (int64_t)device_sms() * 2 * BA_WARPS;
+        const int q_rows = q_items <= warps ? 1 : sizeof(T) == 2 && q_items > 12 * warps ? BA_MANY : BA_ROWS;
         const int64_t qb = (q_items + BA_WARPS * q_rows - 1) / (BA_WARPS * q_rows);
         return launch_ex(block_append_kernel<T, TQ>, dim3((unsigned)(kv + qb + 1)), dim3(BA_THREADS), 0, s, false, pool, geo,
                          R, (unsigned)kv, by_row, q_rows);
