@@ -450,11 +450,18 @@ int kv_append_rope(const kvq_pool *pool, int layer, const float *cos_sin, int n_
 
 /* paged_decode_attn_fp8b, paged_decode_attn_fp8b_combined: single-token
  * attention over an fp8b pool; the same arguments, plan, workspace and results
- * as the entry points of the other formats above.  The combined form merges the
- * units in a second small launch on the same stream; it does not use the
- * workspace's counters, so the workspace needs no initialisation.  Calls on the
- * same workspace must not overlap on the GPU.  A group all of whose pages are
- * out of range gets zeros. */
+ * as the entry points of the other formats above.  q is fp32: of kv_append_rope's
+ * query ask for KVQ_F32.  The combined form merges the units in a second small
+ * launch on the same stream; it does not use the workspace's counters, so the
+ * workspace needs no initialisation.  Calls on the same workspace must not
+ * overlap on the GPU, and outputs must not overlap q.  A group all of whose pages
+ * are out of range gets zeros from the combined form, NaN from attn_combine.  A
+ * captured call holds info's counts: it may be replayed with the bytes of another
+ * plan only where that plan's info is the same.
+ * Q enters the tensor cores as pairs of fp16 under one power of two per head (22
+ * bits), and so do the weights, measured by the largest product of weight and V
+ * scale of each head.  Sums of weights times values are kept in fp32 before the
+ * division: values below 2^100. */
 int paged_decode_attn_fp8b(const kvq_pool *pool, int layer, const float *q, const int32_t *page_table, int max_pages,
                            const int32_t *plan, const kvq_plan_info *info, float *workspace, uint64_t workspace_bytes,
                            int32_t *status, void *stream);
@@ -466,9 +473,12 @@ int paged_decode_attn_fp8b_combined(const kvq_pool *pool, int layer, const float
 /* Plan of a ragged prefill (host only): sequence s brings n_tok[s] >= 0 new
  * tokens at positions pos0[s] .., so its token i attends to the keys
  * 0 .. pos0[s] + i.  The (token, query head) rows of each KV head are taken in
- * tiles of 128, and the plan deals the tiles, or their key ranges in steps of 128
- * keys, to n_ctas CTAs (0 = one per SM of the current device) as evenly as possible;
- * a tile cut between CTAs is merged from partial results in the workspace.  pos0, n_tok:
+ * tiles of 128, whose key ranges are counted in steps of 128 keys.  The plan lays
+ * them end to end and cuts equal shares for n_ctas CTAs (0 = one per SM of the
+ * current device); a tile cut between CTAs is merged from partial results in the
+ * workspace.  Where whole tiles, the longest first to the CTA with the least, take
+ * the longest CTA at most 10 steps more (2 where there are no more tiles than
+ * CTAs), nothing is cut.  pos0, n_tok:
  * host int32 [n_seq], pos0[s] >= 0 and pos0[s] + n_tok[s] <= max_pages * 256.
  * plan, plan_capacity, info: as for kvq_decode_plan (KVQ_ESIZE with
  * info->plan_len set when the array is too small).  KVQ_EUNSUPPORTED for a
@@ -500,15 +510,24 @@ int kvq_prefill_plan(const kvq_pool_desc *desc, int n_seq, const int32_t *pos0, 
  *            for fp32, rounded to 11 bits.  A NaN or an infinity in a row of q
  *            makes that (token, head) NaN and no other.  Scores are fp32; beyond
  *            2^20 in magnitude, where fp32 no longer resolves them, a row's
- *            result may be NaN
+ *            result may be NaN.
+ *            The weights of the values, V scale included, are rounded to fp16 and
+ *            enter as a sum of three E5M2 terms, measured by the row's largest
+ *            product of weight and V scale: 11 bits down to 2^-15 of it, below that
+ *            within 2^-25 of it.  The sum of the weights is fp32 throughout.  So
+ *            rounding them moves a result, out_f32 too, by about 2^-12 of its sum
+ *            of |weight v| at most.
+ *            Sums of weights times values are kept in fp32 before the division:
+ *            values below 2^100
  *  plan      device copy of the kvq_prefill_plan array; info its host info
  *  workspace device, at least info->workspace_bytes (may be NULL when that is 0),
  *            needs no initialisation; calls that share it must not overlap
  *  out_bf16  device [n_rows][n_q_heads][256] bf16 (required); out_f32 the same in
  *            fp32 (optional)
+ * Outputs must not overlap q.
  * A slot out of range sets KVQ_STATUS_BAD_SLOT and its tokens are skipped (a row
  * left with no key gets zeros); a plan entry that does not fit the call sets
- * KVQ_STATUS_BAD_PLAN and its rows are not written. */
+ * KVQ_STATUS_BAD_PLAN and its rows hold no result. */
 int paged_prefill_attn_fp8b(const kvq_pool *pool, int layer, const void *q, int q_dtype, int64_t q_stride,
                             const int32_t *page_table, int max_pages, const int32_t *plan,
                             const kvq_prefill_info *info, float *workspace, uint64_t workspace_bytes,

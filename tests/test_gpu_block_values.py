@@ -258,3 +258,38 @@ def test_decode_takes_the_query_of_an_append():
         for h in range(2):
             want = torch.from_numpy(cache.values(table[b], 1, h)[1].astype(np.float32)).to(torch.bfloat16)
             assert torch.equal(out[b, 6 * h:6 * h + 6].cpu(), want.expand(6, 256))
+
+
+@pytest.mark.parametrize("n_ctas", [1, 148])
+def test_a_sequence_without_pages(n_ctas):
+    """Zeros from the combined decode, NaN where attn_combine divides by no weight at all, and the other sequence as alone."""
+    rng = np.random.default_rng(280)
+    lens = [700, 300]
+    table, n_slots = page_table(rng, lens)
+    cache = random_cache(rng, n_slots, 2)
+    q = rng.standard_normal((2, 12, 256)).astype(np.float32)
+    gone = table.copy()
+    gone[0] = -1
+    for mode in ("combined", "split"):
+        status = i32([0])
+        _, of = decode(make_pool(cache, 12), dev(q), dev(gone), lens, n_ctas=n_ctas, mode=mode, status=status)
+        assert int(status.item()) == kvq.STATUS_BAD_SLOT
+        assert (of[0] == 0).all() if mode == "combined" else torch.isnan(of[0]).all()
+        check_rows(cache, table[1:], [299], [1], dev(q[1:]), of[1:])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_rounding_of_the_weights(dtype):
+    """kvq.h: about 2^-12 of the sum of |weight v|.  Keys of 0 make every weight the same, 1 / n, whatever q is."""
+    rng = np.random.default_rng(290)
+    pos0, toks = [900], [200]
+    table, n_slots = page_table(rng, [1100])
+    cache = random_cache(rng, n_slots, 1)
+    cache.codes[:, :, 0] = 0
+    q = dev(rng.standard_normal((200, 4, 256)).astype(np.float32), DT[dtype])
+    _, of = prefill(make_pool(cache, 4), q, dev(table), pos0, toks)
+    v = cache.values(table[0], 1100, 0)[1]
+    n = np.arange(901, 1101)[:, None]
+    want, B = np.cumsum(v, 0)[900:] / n, np.cumsum(np.abs(v), 0)[900:] / n
+    err = np.abs(of.cpu().numpy().astype(np.float64) - want[:, None])
+    assert (err <= 1.01 * 2.0 ** -12 * B[:, None] + 1e-30).all()
