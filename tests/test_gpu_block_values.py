@@ -84,7 +84,7 @@ def check_rows(cache, table, pos0, toks, q, of, dtype=None):
     hq, hkv, row = q.shape[1], cache.codes.shape[1], 0
     G, qf, got = hq // hkv, q.float().cpu().numpy().astype(np.float64), of.cpu().numpy().astype(np.float64)
     for b, (p0, n) in enumerate(zip(pos0, toks)):
-        for h in range(hkv):
+        for h in range(hkv if n else 0):
             k, v = cache.values(table[b], p0 + n, h)
             d = np.repeat(cache.scales[table[b, :-(-(p0 + n) // 256)], h, :, 1].astype(np.float64).ravel(), 64)[:p0 + n]
             x = qf[row:row + n, h * G:(h + 1) * G].reshape(n * G, 256)
