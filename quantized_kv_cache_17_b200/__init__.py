@@ -424,8 +424,8 @@ def kv_append_rope(pool: KVPool, layer: int, k, v, row_start, pos0, page_table, 
     row_start[s] .. row_start[s+1] - 1 at positions pos0[s] ..; row_start, pos0 and
     page_table are device int32.  Returns the rotated q (q_out, or a new tensor of
     type q_out_dtype: fp32, which every decode takes, or q's own type for fp8b pools,
-    which the prefill takes; by default fp32 except that fp8b keeps q's type; rows
-    past row_start[-1] are not written), None without
+    which the prefill takes; by default fp32 except that fp8b keeps q's type; rows below
+    row_start[0] and from row_start[-1] on are not written), None without
     q.  k and v may both be None."""
     torch = _torch()
     d = pool.desc
